@@ -1,10 +1,12 @@
 """Builds the C-ABI library ``lib/libhsdp_fsdp.so`` in-tree.
 
-Four translation units compiled in parallel and linked with nvcc:
+The translation units are compiled in parallel and linked with nvcc:
   * csrc/fsdp_kernels.cu -- the sm_103a kernels (nvcc, one -gencode)
   * csrc/fsdp_bulk.cu    -- the bulk-fed fused reduce of a capped grid
   * csrc/fsdp_noalloc.cu -- the allocation-free fused gradient sync
+  * csrc/fsdp_embedding.cu, fsdp_dropout.cu, fsdp_norm.cu -- the training operators
   * csrc/fsdp_capi.cpp   -- plan, bindings and entry points (host C++)
+  * csrc/fsdp_ops_capi.cpp -- entry points of the training operators (host C++)
 No fast-math, no FMA contraction, no flush-to-zero: the kernels' additions,
 divisions and conversions are single IEEE operations.
 """
@@ -24,6 +26,9 @@ LIB_NAME = "libhsdp_fsdp.so"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-Wall", "-ftz=false",
               "-prec-div=true", "-prec-sqrt=true", "-fmad=false", "--expt-relaxed-constexpr"]
+CUDA_SOURCES = ["fsdp_kernels.cu", "fsdp_noalloc.cu", "fsdp_bulk.cu", "fsdp_embedding.cu", "fsdp_dropout.cu",
+                "fsdp_norm.cu"]
+CXX_SOURCES = ["fsdp_capi.cpp", "fsdp_ops_capi.cpp"]
 CXX_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra"]
 
 
@@ -47,20 +52,11 @@ def build(verbose: bool = False, extra_nvcc=()) -> str:
     os.makedirs(LIB_DIR, exist_ok=True)
     inc = ["-I", INCLUDE, "-I", CSRC]
     tag = str(os.getpid())
-    obj_k = os.path.join(LIB_DIR, f"fsdp_kernels.{tag}.o")
-    obj_n = os.path.join(LIB_DIR, f"fsdp_noalloc.{tag}.o")
-    obj_b = os.path.join(LIB_DIR, f"fsdp_bulk.{tag}.o")
-    obj_c = os.path.join(LIB_DIR, f"fsdp_capi.{tag}.o")
-    jobs = [
-        [nvcc, *ARCH, *NVCC_FLAGS, *extra_nvcc, *inc, "-c", os.path.join(CSRC, "fsdp_kernels.cu"),
-         "-o", obj_k],
-        [nvcc, *ARCH, *NVCC_FLAGS, *extra_nvcc, *inc, "-c", os.path.join(CSRC, "fsdp_noalloc.cu"),
-         "-o", obj_n],
-        [nvcc, *ARCH, *NVCC_FLAGS, *extra_nvcc, *inc, "-c", os.path.join(CSRC, "fsdp_bulk.cu"),
-         "-o", obj_b],
-        ["g++", *CXX_FLAGS, *inc, "-I", os.path.join(cuda, "include"), "-c",
-         os.path.join(CSRC, "fsdp_capi.cpp"), "-o", obj_c],
-    ]
+    obj = {f: os.path.join(LIB_DIR, f"{os.path.splitext(f)[0]}.{tag}.o") for f in CUDA_SOURCES + CXX_SOURCES}
+    jobs = [[nvcc, *ARCH, *NVCC_FLAGS, *extra_nvcc, *inc, "-c", os.path.join(CSRC, f), "-o", obj[f]]
+            for f in CUDA_SOURCES]
+    jobs += [["g++", *CXX_FLAGS, *inc, "-I", os.path.join(cuda, "include"), "-c", os.path.join(CSRC, f), "-o", obj[f]]
+             for f in CXX_SOURCES]
     procs = [subprocess.Popen(j, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True) for j in jobs]
     failed = []
     for j, p in zip(jobs, procs):
@@ -72,10 +68,10 @@ def build(verbose: bool = False, extra_nvcc=()) -> str:
     if failed:
         raise RuntimeError("compile failed: " + "; ".join(failed))
     tmp = os.path.join(LIB_DIR, f"{LIB_NAME}.{tag}")
-    subprocess.run([nvcc, *ARCH, "-shared", "-cudart", "shared", obj_k, obj_n, obj_b, obj_c, "-o", tmp,
+    subprocess.run([nvcc, *ARCH, "-shared", "-cudart", "shared", *obj.values(), "-o", tmp,
                     "-Xlinker", "-rpath," + os.path.join(cuda, "lib64")], check=True)
     os.replace(tmp, library_path())
-    for o in (obj_k, obj_n, obj_b, obj_c):
+    for o in obj.values():
         os.remove(o)
     return library_path()
 

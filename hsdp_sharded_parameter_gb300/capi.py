@@ -20,6 +20,7 @@ from .build import library_path
 FSDP_OK, FSDP_ERR_INVALID_ARG, FSDP_ERR_NOT_IMPLEMENTED, FSDP_ERR_CUDA, FSDP_ERR_NOMEM = range(5)
 FSDP_F32, FSDP_BF16 = 0, 1
 FSDP_AVG, FSDP_SUM = 0, 1
+FSDP_I32, FSDP_I64 = 0, 1
 FSDP_STATUS_PRODUCER_WAIT, FSDP_STATUS_CONSUMER_WAIT, FSDP_STATUS_ORDER = 1, 2, 4
 (FSDP_ROLE_SHARDS, FSDP_ROLE_AG_OUTPUT, FSDP_ROLE_FULL_PARAMS, FSDP_ROLE_GRADS,
  FSDP_ROLE_RS_INPUT, FSDP_ROLE_FUSED, FSDP_ROLE_SHARD_GRADS) = range(7)
@@ -93,6 +94,16 @@ def lib():
         L.fsdp_ar_reduce.argtypes = [vp, vp, i32, vp]
         L.fsdp_rs_ar_reduce_noalloc.argtypes = [vp, i32, vp, vp, vp]
         L.fsdp_ag_unshard.argtypes = [vp, vp, vp, vp]
+        f64, u32, u64, sz = ctypes.c_double, ctypes.c_uint32, ctypes.c_uint64, ctypes.c_size_t
+        L.fsdp_embedding.argtypes = [i32, vp, i64, i64, i64, i32, vp, i64, i64, f64, i32, vp, i64, vp]
+        L.fsdp_embedding_grad_workspace.argtypes = [i64, i64, i64, P(sz)]
+        L.fsdp_embedding_grad.argtypes = [i32, vp, i64, i32, vp, i64, i64, f64, i32, i32, vp, i64, i64, i64, vp, sz, vp]
+        L.fsdp_dropout.argtypes = [i64, i64, i32, vp, i64, vp, i64, f64, u64, u32, vp, i64, vp]
+        L.fsdp_layer_norm.argtypes = [i64, i64, i32, vp, i64, vp, i64, f64, u64, u32, i32, vp, vp, f64, vp, i64, vp,
+                                      i64, vp, vp, vp]
+        L.fsdp_layer_norm_grad_workspace.argtypes = [i64, i64, P(sz)]
+        L.fsdp_layer_norm_grad.argtypes = [i64, i64, i32, vp, i64, vp, i64, vp, i64, vp, vp, i32, vp, f64, u64, u32,
+                                           i32, vp, i64, vp, i64, i32, vp, vp, vp, sz, vp]
         _lib = L
     return _lib
 
@@ -345,3 +356,195 @@ def fsdp_rs_ar_reduce_noalloc(plan, grad_dt, grads, fused, stream=None):
     f = (ctypes.c_void_p * max(len(fused), 1))(*[t.data_ptr() for t in fused])
     _check(lib().fsdp_rs_ar_reduce_noalloc(plan.handle, DTYPES.get(grad_dt, grad_dt), g, f,
                                            _stream(stream)))
+
+
+# --------------------------------------------------------- training operators
+#
+# Tensors are passed as they are: matrices of 2 dimensions with any row
+# stride and neighbouring columns, or contiguous tensors of any other number
+# of dimensions, the last being the columns. Outputs and workspaces are the
+# caller's. Operators run on the current device and, by default, its current
+# stream; on another stream the caller orders the tensors' other uses.
+
+_TYPES = {}
+
+
+def _types():
+    """torch dtypes of the operators' values and of their ids, as the C ABI's."""
+    import torch
+
+    _TYPES.update({torch.float32: FSDP_F32, torch.bfloat16: FSDP_BF16})
+    _TYPES["ids"] = {torch.int32: FSDP_I32, torch.int64: FSDP_I64}
+    _TYPES["device"] = torch.cuda.current_device
+    return _TYPES
+
+
+def _refuse(what, why):
+    raise FsdpError(FSDP_ERR_INVALID_ARG, f"{what}: {why}")
+
+
+def _matrix(what, name, t):
+    """(pointer, rows, columns, row stride, dtype, device) of a tensor."""
+    shape, strides = t.shape, t.stride()
+    n = len(shape)
+    dt = (_TYPES or _types()).get(t.dtype)
+    if dt is None or not t.is_cuda:
+        _refuse(what, f"{name} is {t.dtype} on {t.device}; expected float32 or bfloat16 on a GPU")
+    if n == 2:
+        rows, cols = shape
+        stride = strides[0]
+        if strides[1] != 1 and cols > 1:
+            _refuse(what, f"{name}'s columns are not neighbours in memory (strides {tuple(strides)})")
+    else:
+        if n == 0 or not t.is_contiguous():
+            _refuse(what, f"{name} is neither a matrix nor contiguous")
+        cols = stride = shape[-1]
+        rows = t.numel() // cols if cols else 0
+    return t.data_ptr(), rows, cols, stride, dt, t.get_device()
+
+
+def _like(what, name, t, rows, cols, dt, dev):
+    """Pointer and row stride of a tensor that has to match these, (None, 0) of None."""
+    if t is None:
+        return None, 0
+    p, r, c, stride, d, v = _matrix(what, name, t)
+    if r != rows or c != cols or (d != dt and dt is not None) or v != dev:
+        _refuse(what, f"{name} is {r} x {c} {t.dtype} on {t.device}; expected {rows} x {cols} "
+                      f"{_torch_dtype(dt) if dt is not None else ''} on cuda:{dev}")
+    return p, stride
+
+
+def _on(what, dev):
+    if dev != _TYPES["device"]():
+        _refuse(what, f"the tensors are on cuda:{dev}, which is not the current device")
+
+
+def _vector(what, name, t, n, dev, dtype=None):
+    """(pointer, dtype) of a contiguous vector of n values, (None, None) of None."""
+    if t is None:
+        return None, None
+    dt = _TYPES.get(t.dtype)
+    if dt is None or (dtype is not None and dt != dtype) or t.numel() != n or not t.is_contiguous() or t.get_device() != dev:
+        _refuse(what, f"{name} is {tuple(t.shape)} {t.dtype} on {t.device}; expected {n} contiguous values of "
+                      f"{'float32 or bfloat16' if dtype is None else _torch_dtype(dtype)} on cuda:{dev}")
+    return t.data_ptr(), dt
+
+
+def _pair(what, names, a, b, n, dev):
+    """Pointers and the common dtype of two optional parameter vectors."""
+    pa, da = _vector(what, names[0], a, n, dev)
+    pb, db = _vector(what, names[1], b, n, dev, da)
+    return pa, pb, da if da is not None else (db if db is not None else FSDP_F32)
+
+
+def _ids(what, ids, dev):
+    t = _TYPES["ids"].get(ids.dtype)
+    if t is None or not ids.is_contiguous() or ids.get_device() != dev:
+        _refuse(what, f"ids is {ids.dtype} on {ids.device}; expected contiguous int32 or int64 on cuda:{dev}")
+    return t, ids.data_ptr(), ids.numel()
+
+
+def _work(what, t, dev):
+    if not t.is_contiguous() or t.get_device() != dev:
+        _refuse(what, f"workspace is not a contiguous tensor on cuda:{dev}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def fsdp_embedding(table, ids, out, scale=1.0, first_row=0, stream=None):
+    """out[t] = scale * table[ids[t] - first_row], zeros where the id names no
+    row of the table. table: (vocab, cols); ids: n int32 or int64; out:
+    (n, cols), float32 or bfloat16 whatever the table's type."""
+    what = "embedding"
+    tp, vocab, cols, ts, tdt, dev = _matrix(what, "table", table)
+    it, ip, n = _ids(what, ids, dev)
+    op, rows, ocols, os_, odt, odev = _matrix(what, "out", out)
+    if n and (rows != n or ocols != cols) or odev != dev:
+        _refuse(what, f"out is {rows} x {ocols} on cuda:{odev}; expected {n} x {cols} on cuda:{dev}")
+    _on(what, dev)
+    _check(lib().fsdp_embedding(tdt, tp, ts, vocab, cols, it, ip, n, first_row, scale, odt, op, os_, _stream(stream)))
+
+
+def fsdp_embedding_grad_workspace(n_ids, vocab, cols):
+    """Bytes of the workspace that fsdp_embedding_grad needs."""
+    b = ctypes.c_size_t()
+    _check(lib().fsdp_embedding_grad_workspace(n_ids, vocab, cols, ctypes.byref(b)))
+    return b.value
+
+
+def fsdp_embedding_grad(grad_out, ids, grad_table, workspace, scale=1.0, first_row=0, accumulate=False, stream=None):
+    """grad_table[v] = scale * sum of grad_out[t] over the tokens t that name
+    row v, in ascending order of t; zeros where there is none. With accumulate,
+    added to what grad_table holds. workspace: a tensor of at least
+    fsdp_embedding_grad_workspace(n, vocab, cols) bytes."""
+    what = "embedding_grad"
+    gp, rows, cols, gs, gdt, dev = _matrix(what, "grad_out", grad_out)
+    it, ip, n = _ids(what, ids, dev)
+    tp, vocab, tcols, ts, tdt, tdev = _matrix(what, "grad_table", grad_table)
+    if n and (rows != n or cols != tcols) or tdev != dev:
+        _refuse(what, f"grad_out is {rows} x {cols}, ids {n}, grad_table {vocab} x {tcols} on cuda:{tdev}")
+    wp, wb = _work(what, workspace, dev)
+    _on(what, dev)
+    _check(lib().fsdp_embedding_grad(gdt, gp, gs, it, ip, n, first_row, scale, int(accumulate), tdt, tp, ts, vocab,
+                                     tcols, wp, wb, _stream(stream)))
+
+
+def fsdp_dropout(x, out, p, seed, draw=0, residual=None, stream=None):
+    """out = residual + dropout(x): an element of row r and column c is kept,
+    and scaled, by a mask that (seed, draw, r, c) give and nothing stores. The
+    backward pass is this call on the gradient. out may be x or residual."""
+    what = "dropout"
+    xp, rows, cols, xs, dt, dev = _matrix(what, "x", x)
+    rp, rs = _like(what, "residual", residual, rows, cols, dt, dev)
+    op, os_ = _like(what, "out", out, rows, cols, dt, dev)
+    _on(what, dev)
+    _check(lib().fsdp_dropout(rows, cols, dt, xp, xs, rp, rs, p, seed, draw, op, os_, _stream(stream)))
+
+
+def fsdp_layer_norm(x, weight, bias, out, mean, rstd, eps=1e-5, residual=None, hidden=None, p=0.0, seed=0, draw=0,
+                    stream=None):
+    """out = layer norm of the rows of h = residual + dropout(x) (no residual,
+    p = 0: of x), times weight plus bias (either may be None). hidden receives
+    h, mean and rstd (float32) each row's; any of the three may be None."""
+    what = "layer_norm"
+    xp, rows, cols, xs, dt, dev = _matrix(what, "x", x)
+    rp, rs = _like(what, "residual", residual, rows, cols, dt, dev)
+    hp, hs = _like(what, "hidden", hidden, rows, cols, dt, dev)
+    op, os_ = _like(what, "out", out, rows, cols, dt, dev)
+    wp, bp, pdt = _pair(what, ("weight", "bias"), weight, bias, cols, dev)
+    mp, _ = _vector(what, "mean", mean, rows, dev, FSDP_F32)
+    sp, _ = _vector(what, "rstd", rstd, rows, dev, FSDP_F32)
+    _on(what, dev)
+    _check(lib().fsdp_layer_norm(rows, cols, dt, xp, xs, rp, rs, p, seed, draw, pdt, wp, bp, eps, hp, hs, op, os_, mp,
+                                 sp, _stream(stream)))
+
+
+def fsdp_layer_norm_grad_workspace(rows, cols):
+    """Bytes of the workspace that fsdp_layer_norm_grad needs."""
+    b = ctypes.c_size_t()
+    _check(lib().fsdp_layer_norm_grad_workspace(rows, cols, ctypes.byref(b)))
+    return b.value
+
+
+def fsdp_layer_norm_grad(grad_out, hidden, mean, rstd, weight, grad_x, grad_weight, grad_bias, workspace,
+                         grad_hidden=None, grad_residual=None, p=0.0, seed=0, draw=0, accumulate=False, stream=None):
+    """Gradient of fsdp_layer_norm from its hidden (x where it had neither
+    residual nor dropout), mean and rstd: grad_x, grad_residual (the same
+    before the dropout; may be None), grad_weight and grad_bias (either may be
+    None; with accumulate, added to what they hold). grad_hidden is the
+    gradient that reaches hidden past the norm. workspace: a tensor of at least
+    fsdp_layer_norm_grad_workspace(rows, cols) bytes."""
+    what = "layer_norm_grad"
+    gp, rows, cols, gs, dt, dev = _matrix(what, "grad_out", grad_out)
+    hp, hs = _like(what, "hidden", hidden, rows, cols, dt, dev)
+    ap, as_ = _like(what, "grad_hidden", grad_hidden, rows, cols, dt, dev)
+    rp, rs = _like(what, "grad_residual", grad_residual, rows, cols, dt, dev)
+    xp, xs = _like(what, "grad_x", grad_x, rows, cols, dt, dev)
+    mp, _ = _vector(what, "mean", mean, rows, dev, FSDP_F32)
+    sp, _ = _vector(what, "rstd", rstd, rows, dev, FSDP_F32)
+    wp, wdt = _vector(what, "weight", weight, cols, dev)
+    dwp, dbp, gdt = _pair(what, ("grad_weight", "grad_bias"), grad_weight, grad_bias, cols, dev)
+    kp, kb = _work(what, workspace, dev)
+    _on(what, dev)
+    _check(lib().fsdp_layer_norm_grad(rows, cols, dt, gp, gs, ap, as_, hp, hs, mp, sp, FSDP_F32 if wdt is None else wdt,
+                                      wp, p, seed, draw, int(accumulate), rp, rs, xp, xs, gdt, dwp, dbp, kp, kb,
+                                      _stream(stream)))

@@ -1,0 +1,83 @@
+// Launch interface of the training operators (embedding, dropout, layer
+// norm): what the C-ABI entry points (fsdp_ops_capi.cpp) hand to the kernels
+// once the arguments are checked. Not installed.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "hsdp_fsdp.h"
+
+namespace fsdp {
+
+// A matrix in device memory: element (r, c) at data[r * stride + c].
+struct Mat {
+    void* data;
+    int64_t stride;
+};
+
+// The mask of a dropout. limit 65536: nothing is dropped.
+struct Mask {
+    uint32_t key0, key1, draw, limit;
+    float scale;  // 65536 / limit
+};
+
+struct EmbeddingArgs {
+    Mat table, out;
+    const void* ids;
+    int64_t vocab, cols, n, first;
+    int wide_ids;  // 1: 64-bit ids
+    float scale;
+};
+
+struct EmbeddingGradArgs {
+    Mat grad, table;
+    const void* ids;
+    int64_t vocab, cols, n, first;
+    int wide_ids, accumulate;
+    float scale;
+    void* work;
+};
+
+struct DropoutArgs {
+    int64_t rows, cols;
+    Mat x, res, out;  // res.data may be nullptr
+    Mask mask;
+};
+
+struct NormArgs {
+    int64_t rows, cols;
+    Mat x, res, hidden, out;  // res.data, hidden.data may be nullptr
+    const void *weight, *bias;
+    float *mean, *rstd;
+    float eps;
+    Mask mask;
+};
+
+struct NormGradArgs {
+    int64_t rows, cols;
+    Mat grad, grad_hidden, hidden, grad_res, grad_x;
+    const float *mean, *rstd;
+    const void* weight;
+    void *grad_weight, *grad_bias;
+    int accumulate;
+    float* work;
+    Mask mask;
+};
+
+// SMs of the current device.
+int sm_count();
+
+size_t embedding_grad_bytes(int64_t n, int64_t vocab, int64_t cols);
+size_t norm_grad_bytes(int64_t rows, int64_t cols);
+
+// Each enqueues its kernels (counting them) and returns the launches' error.
+cudaError_t launch_embedding(int table_dt, int out_dt, const EmbeddingArgs& a, cudaStream_t s);
+cudaError_t launch_embedding_grad(int grad_dt, int table_dt, const EmbeddingGradArgs& a, cudaStream_t s);
+cudaError_t launch_dropout(int dt, const DropoutArgs& a, cudaStream_t s);
+cudaError_t launch_norm(int dt, int param_dt, const NormArgs& a, cudaStream_t s);
+cudaError_t launch_norm_grad(int dt, int param_dt, int param_grad_dt, const NormGradArgs& a, cudaStream_t s);
+
+}  // namespace fsdp

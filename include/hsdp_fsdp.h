@@ -57,6 +57,7 @@
 #ifndef HSDP_FSDP_H
 #define HSDP_FSDP_H
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
@@ -387,6 +388,106 @@ int fsdp_rs_ar_reduce_apply(fsdp_plan_t plan, fsdp_binding_t grads, fsdp_binding
  * buffer's size here. Returns as fsdp_rs_ar_reduce does. */
 int fsdp_rs_ar_reduce_noalloc(fsdp_plan_t plan, int grad_dtype, const void* const* grads,
                               float* const* fused, fsdp_stream_t stream);
+
+/* -------------------------------------------------- training operators */
+
+/* Operators that use the full parameters an unshard gathers and write the
+ * full gradients a gradient sync reduces: embedding lookup, dropout and layer
+ * norm, forward and backward. The pages leave the model to the caller and
+ * have no counterpart; the operators exist for this library's users. They
+ * need no plan, work on the current device, and follow the conventions at
+ * the head of this file, except that a backward pass enqueues up to three
+ * kernels and takes its scratch memory from the caller: a device buffer,
+ * 16-byte aligned, of the size its _workspace function gives; calls that may
+ * overlap on the GPU need workspaces of their own. Nothing in a workspace is
+ * read before it is written, and nothing is kept there between calls.
+ *
+ * Matrices: element (r, c) sits at data[r * stride + c]; strides count
+ * elements. An input's stride may be any value >= 0 (0: every row the same);
+ * an output's is at least its columns. An output may overlap no other
+ * operand unless the call says so. Pointers are aligned to their element
+ * size; every alignment, stride and number of columns is computed in full,
+ * and 16-byte aligned rows are the fast ones. Zero rows or columns are
+ * allowed: sums over no rows are zero.
+ *
+ * Numerics: everything between an operator's inputs and outputs is computed
+ * and summed in binary32 and rounded once to the output's type. Sums are
+ * taken in an order fixed by the sizes, so equal calls give equal bits. */
+
+enum fsdp_index_type { FSDP_I32 = 0, FSDP_I64 = 1 };
+
+/* Embedding lookup: out[t] = scale * table[ids[t] - first_row] for t < n_ids,
+ * cast to out_dt. An id outside [first_row, first_row + vocab) names no row
+ * and gives a row of zeros: padding tokens (-1, say), or, with first_row set
+ * on a table that holds a slice of the vocabulary, tokens of other slices.
+ * vocab, n_ids < 2^31 - 1. */
+int fsdp_embedding(int table_dt, const void* table, int64_t table_stride, int64_t vocab, int64_t cols,
+                   int index_type, const void* ids, int64_t n_ids, int64_t first_row, double scale,
+                   int out_dt, void* out, int64_t out_stride, fsdp_stream_t stream);
+
+/* Scratch bytes of fsdp_embedding_grad. */
+int fsdp_embedding_grad_workspace(int64_t n_ids, int64_t vocab, int64_t cols, size_t* bytes);
+
+/* Gradient of the lookup: grad_table[v] = scale * sum over t with
+ * ids[t] - first_row = v of grad_out[t], the tokens of a row taken in
+ * ascending order after a stable sort; rows that no token names become zero,
+ * and tokens that name no row are left out. With accumulate != 0 the result
+ * is added, in binary32, to what grad_table holds and rounded once, and rows
+ * that no token names are not touched (gradient accumulation; an embedding
+ * tied to an output projection). */
+int fsdp_embedding_grad(int grad_dt, const void* grad_out, int64_t grad_out_stride, int index_type,
+                        const void* ids, int64_t n_ids, int64_t first_row, double scale, int accumulate,
+                        int table_dt, void* grad_table, int64_t grad_table_stride, int64_t vocab,
+                        int64_t cols, void* workspace, size_t workspace_bytes, fsdp_stream_t stream);
+
+/* Dropout with a mask that is never stored: out = residual + keep * x *
+ * 65536 / K, where K = round((1 - p) * 65536) and a dropped element adds
+ * exactly 0, whatever x holds there. residual may be NULL (0). The mask is a
+ * function of (seed, draw, r, c) alone: Philox4x32-10 (Salmon, Moraes, Dror,
+ * Shaw 2011) with the counter (c / 8, low word of r, high word of r, draw)
+ * and the key (low, high word of seed) gives the 16-bit halves of its four
+ * words, low half first, to columns c / 8 * 8 ... + 7; an element is kept
+ * when its half is below K. p in [0, 1] acts in steps of 2^-16, the scale
+ * with it, so the expectation is exact. The backward pass is this call on
+ * the gradient with the same p, seed and draw. out may be x or residual
+ * themselves (same pointer and stride). cols <= 2^34. */
+int fsdp_dropout(int64_t rows, int64_t cols, int dt, const void* x, int64_t x_stride, const void* residual,
+                 int64_t residual_stride, double p, uint64_t seed, uint32_t draw, void* out,
+                 int64_t out_stride, fsdp_stream_t stream);
+
+/* Layer norm of each row of h = residual + dropout(x) (see fsdp_dropout;
+ * residual NULL and p = 0: h = x): out = (h - mean) * rstd * weight + bias,
+ * mean = sum h / cols, rstd = 1 / sqrt(sum (h - mean)^2 / cols + eps), from h
+ * before any rounding. weight (NULL: 1) and bias (NULL: 0) hold cols elements
+ * of param_dt. hidden, when not NULL, receives h; mean and rstd, when not
+ * NULL, rows values each. All matrices have dtype dt. */
+int fsdp_layer_norm(int64_t rows, int64_t cols, int dt, const void* x, int64_t x_stride,
+                    const void* residual, int64_t residual_stride, double p, uint64_t seed, uint32_t draw,
+                    int param_dt, const void* weight, const void* bias, double eps, void* hidden,
+                    int64_t hidden_stride, void* out, int64_t out_stride, float* mean, float* rstd,
+                    fsdp_stream_t stream);
+
+/* Scratch bytes of fsdp_layer_norm_grad. */
+int fsdp_layer_norm_grad_workspace(int64_t rows, int64_t cols, size_t* bytes);
+
+/* Gradient of fsdp_layer_norm from hidden (its h; x where it had neither
+ * residual nor dropout), mean and rstd. With g = grad_out * weight and
+ * u = (hidden - mean) * rstd, the gradient of h is
+ *   t = rstd * (g - sum(g) / cols - u * sum(g * u) / cols) + grad_hidden,
+ * grad_hidden being the gradient that reaches h past the norm (the residual
+ * stream's; NULL: 0). grad_residual (may be NULL) = t, grad_x = the dropout of
+ * t (t itself for p = 0); grad_weight = sum over rows of grad_out * u,
+ * grad_bias = sum over rows of grad_out, cols elements of param_grad_dt each,
+ * either or both NULL. With accumulate != 0 both are added, in binary32, to
+ * what is there and rounded once. grad_x and grad_residual are always
+ * overwritten. */
+int fsdp_layer_norm_grad(int64_t rows, int64_t cols, int dt, const void* grad_out, int64_t grad_out_stride,
+                         const void* grad_hidden, int64_t grad_hidden_stride, const void* hidden,
+                         int64_t hidden_stride, const float* mean, const float* rstd, int param_dt,
+                         const void* weight, double p, uint64_t seed, uint32_t draw, int accumulate,
+                         void* grad_residual, int64_t grad_residual_stride, void* grad_x,
+                         int64_t grad_x_stride, int param_grad_dt, void* grad_weight, void* grad_bias,
+                         void* workspace, size_t workspace_bytes, fsdp_stream_t stream);
 
 #ifdef __cplusplus
 }
