@@ -7,42 +7,62 @@ namespace fsdp {
 namespace {
 
 constexpr int kDropWarps = 8;
-
-// A warp takes a span of 256 columns of a row at a time, kGroup of them in
-// flight.
+// Spans of a warp at a time.
 template <typename T>
-__global__ void __launch_bounds__(32 * kDropWarps) dropout_kernel(DropoutArgs a, int64_t spans, int64_t items) {
+constexpr int kDropSpans = sizeof(T) == 4 ? 2 : 4;
+
+// A warp takes kU neighbouring spans of 256 columns of a row at a time and
+// loads them all before it draws the first mask.
+template <typename T, bool kAligned>
+__global__ void __launch_bounds__(32 * kDropWarps, 4) dropout_kernel(DropoutArgs a, int64_t steps, int64_t items) {
+    constexpr int kU = kDropSpans<T>;
     const int lane = threadIdx.x & 31;
     for (int64_t it = warp_id(); it < items; it += warp_count()) {
-        const int64_t row = it / spans, g = (it - row * spans) * 32 + lane, c = g * kGran;
-        const int n = granule_cols(g, a.cols);
-        Raw<T> in, out;
-        float x[8], y[8];
-        load_granule(in, static_cast<const T*>(a.x.data) + row * a.x.stride, c, n);
-        if (a.res.data) load_granule(out, static_cast<const T*>(a.res.data) + row * a.res.stride, c, n);
-        widen(in, x);
-        drop(x, a.mask, row, (uint32_t)g);
-        if (a.res.data) {
-            widen(out, y);
+        const int64_t row = it / steps, g0 = (it - row * steps) * (kU * 32) + lane;
+        const T* x = static_cast<const T*>(a.x.data) + row * a.x.stride;
+        const T* res = static_cast<const T*>(a.res.data) + row * a.res.stride;
+        T* out = static_cast<T*>(a.out.data) + row * a.out.stride;
+        Raw<T> in[kU], add[kU];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] += y[e];
+        for (int u = 0; u < kU; ++u) {
+            const int64_t g = g0 + u * 32;
+            const int n = granule_cols(g, a.cols);
+            load_cols<kAligned>(in[u], x, g * kGran, n);
+            if (a.res.data) load_cols<kAligned>(add[u], res, g * kGran, n);
         }
-        narrow(x, out);
-        store_span(static_cast<T*>(a.out.data) + row * a.out.stride + c, out, n, lane);
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int64_t g = g0 + u * 32;
+            const Cols v = widened(in[u]);
+            Cols y = a.res.data ? widened(add[u]) : all(0.0f);
+            if (a.mask.drops)
+                add_dropped(y, v, a.mask, row, (uint32_t)g);
+            else
+                y = y + v;
+            round_to(y, in[u]);
+            store_cols<kAligned>(out + g * kGran, in[u], granule_cols(g, a.cols), lane);
+        }
     }
+}
+
+template <typename T, bool kAligned>
+void dropout(const DropoutArgs& a, cudaStream_t s) {
+    const int64_t span = kSpan * kDropSpans<T>, steps = (a.cols + span - 1) / span, items = steps * a.rows;
+    const int64_t blocks = (items + kDropWarps - 1) / kDropWarps;
+    const unsigned grid = (unsigned)(blocks < 0x7fffffff ? blocks : 0x7fffffff);
+    dropout_kernel<T, kAligned><<<grid, 32 * kDropWarps, 0, s>>>(a, steps, items);
 }
 
 }  // namespace
 
 cudaError_t launch_dropout(int dt, const DropoutArgs& a, cudaStream_t s) {
     if (a.rows == 0 || a.cols == 0) return cudaSuccess;
-    const int64_t spans = (a.cols + kSpan - 1) / kSpan, items = spans * a.rows;
-    const int64_t blocks = (items + kDropWarps - 1) / kDropWarps;
-    const unsigned grid = (unsigned)(blocks < 0x7fffffff ? blocks : 0x7fffffff);
+    const int es = dt == FSDP_F32 ? 4 : 2;
+    const bool aligned = a.cols % kGran == 0 && on_grid(a.x, es) && on_grid(a.res, es) && on_grid(a.out, es);
     if (dt == FSDP_F32)
-        dropout_kernel<float><<<grid, 32 * kDropWarps, 0, s>>>(a, spans, items);
+        aligned ? dropout<float, true>(a, s) : dropout<float, false>(a, s);
     else
-        dropout_kernel<uint16_t><<<grid, 32 * kDropWarps, 0, s>>>(a, spans, items);
+        aligned ? dropout<uint16_t, true>(a, s) : dropout<uint16_t, false>(a, s);
     count_launch();
     return cudaGetLastError();
 }

@@ -41,11 +41,7 @@ __global__ void __launch_bounds__(32 * kEmbWarps) embedding_kernel(EmbeddingArgs
         Raw<D> out;
         zero_raw(in);
         if (row < a.vocab) load_granule(in, static_cast<const S*>(a.table.data) + row * a.table.stride, c, n);
-        float x[8];
-        widen(in, x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = row < a.vocab ? x[e] * a.scale : 0.0f;
-        narrow(x, out);
+        round_to(row < a.vocab ? widened(in) * all(a.scale) : all(0.0f), out);
         store_span(static_cast<D*>(a.out.data) + t * a.out.stride + c, out, n, lane);
     }
 }
@@ -258,28 +254,28 @@ __global__ void __launch_bounds__(kSortThreads)
 // Scales a row's sums, adds what the table holds where the caller wants it,
 // rounds and stores them.
 template <typename D>
-__device__ __forceinline__ void store_row(const EmbeddingGradArgs& a, int row, int64_t g, float (&x)[8], int lane) {
+__device__ __forceinline__ void store_row(const EmbeddingGradArgs& a, int row, int64_t g, Cols x, int lane) {
     const int n = granule_cols(g, a.cols);
     D* p = static_cast<D*>(a.table.data) + row * a.table.stride + g * kGran;
     Raw<D> r;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] *= a.scale;
+    x = x * all(a.scale);
     if (a.accumulate) {
-        float y[8];
         load_granule(r, p - g * kGran, g * kGran, n);
-        widen(r, y);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] += y[e];
+        x = x + widened(r);
         __syncwarp();  // a shifted load reads its neighbours' blocks
     }
-    narrow(x, r);
+    round_to(x, r);
     store_span(p, r, n, lane);
 }
 
-__device__ __forceinline__ void store_part(float* p, const float (&x)[8]) {
+__device__ __forceinline__ void store_part(float* p, const Cols& x) {
     float4* q = reinterpret_cast<float4*>(p);
-    q[0] = make_float4(x[0], x[1], x[2], x[3]);
-    q[1] = make_float4(x[4], x[5], x[6], x[7]);
+    q[0] = make_float4(x.p[0].x, x.p[0].y, x.p[1].x, x.p[1].y);
+    q[1] = make_float4(x.p[2].x, x.p[2].y, x.p[3].x, x.p[3].y);
+}
+__device__ __forceinline__ Cols load_part(const float* p) {
+    const float4 u = __ldcg(reinterpret_cast<const float4*>(p)), v = __ldcg(reinterpret_cast<const float4*>(p) + 1);
+    return {{make_float2(u.x, u.y), make_float2(u.z, u.w), make_float2(v.x, v.y), make_float2(v.z, v.w)}};
 }
 
 template <typename S, typename D>
@@ -297,7 +293,7 @@ __global__ void __launch_bounds__(32 * kEmbWarps)
     const int n = granule_cols(g, a.cols);
     const int prev = lo > 0 ? __ldg(rows + lo - 1) : -1;
     const int next = hi < count ? __ldg(rows + hi) : -1;
-    float acc[8] = {};
+    Cols acc = all(0.0f);
     int cur = -1;
     bool open = false;  // cur began in an earlier chunk
     for (int b = (int)lo; b < hi; b += 32) {
@@ -314,8 +310,7 @@ __global__ void __launch_bounds__(32 * kEmbWarps)
             for (int u = 0; u < kU; ++u) {
                 if (j + u >= m) break;
                 const int row = __shfl_sync(kFull, my_row, (j + u) & 31);
-                float x[8];
-                widen(in[u], x);
+                const Cols x = widened(in[u]);
                 if (row != cur) {
                     if (cur >= 0) {
                         if (!open)
@@ -325,11 +320,9 @@ __global__ void __launch_bounds__(32 * kEmbWarps)
                     }
                     open = cur < 0 && row == prev;
                     cur = row;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) acc[e] = x[e];
+                    acc = x;
                 } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) acc[e] += x[e];
+                    acc = acc + x;
                 }
             }
         }
@@ -368,24 +361,16 @@ __global__ void __launch_bounds__(32 * kEmbWarps)
         // partial sums b - 1 (its tail), b, ..., last, a share for each warp
         const int64_t last = lo / w.chunk, parts = last - b + 2;
         const int64_t p0 = parts * warp / kEmbWarps, p1 = parts * (warp + 1) / kEmbWarps;
-        float acc[8] = {};
+        Cols acc = all(0.0f);
         if (n)
-            for (int64_t p = p0; p < p1; ++p) {
-                const float4* q = reinterpret_cast<const float4*>(
-                    w.part + (p == 0 ? w.nchunks + b - 1 : b - 1 + p) * w.stride + c);
-                const float4 u = __ldcg(q), v = __ldcg(q + 1);
-                acc[0] += u.x; acc[1] += u.y; acc[2] += u.z; acc[3] += u.w;
-                acc[4] += v.x; acc[5] += v.y; acc[6] += v.z; acc[7] += v.w;
-            }
+            for (int64_t p = p0; p < p1; ++p)
+                acc = acc + load_part(w.part + (p == 0 ? w.nchunks + b - 1 : b - 1 + p) * w.stride + c);
         store_part(&part[warp][lane * kGran], acc);
         __syncthreads();
         if (warp == 0) {
+            for (int q = 1; q < kEmbWarps; ++q)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float s = 0.0f;
-                for (int q = 0; q < kEmbWarps; ++q) s += part[q][lane * kGran + e];
-                acc[e] = s;
-            }
+                for (int e = 0; e < 8; ++e) acc.set(e, acc.get(e) + part[q][lane * kGran + e]);
             store_row<D>(a, row, g, acc, lane);
         }
         __syncthreads();

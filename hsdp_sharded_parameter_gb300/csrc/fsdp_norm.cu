@@ -9,438 +9,679 @@
 // Gradient: with g = grad_out * weight and u = (h - mean) * rstd,
 //   t = rstd * (g - mean(g) - u * mean(g * u)) + grad_hidden,
 // and each thread keeps its columns' sums of grad_out * u and grad_out over
-// the rows its group takes; a second kernel adds the groups' sums.
+// the rows its group takes; a second kernel adds the blocks' sums.
+//
+// Rows in registers: V granules of 8 columns a thread, gw warps a row, blocks
+// that take rows in turn. Each warp copies its spans of the next rows' inputs
+// into shared memory, `depth` rows ahead, so that the loads in flight do not
+// depend on how many warps fit beside the row's registers.
 #include "fsdp_ops.cuh"
 
 namespace fsdp {
 namespace {
 
-constexpr int kNormThreads = 512;  // largest block
-constexpr int kMaxVec = 4;         // granules of a thread
-constexpr int kNormCols = kNormThreads * kMaxVec * kGran;  // widest row kept in registers
+constexpr int kWarps = 16;  // largest block
+constexpr int kWideThreads = 512;
+constexpr int kNormCols = kWarps * 4 * kSpan;  // widest row kept in registers
 
-// Sums two values over a row's group of gw warps; warp is the one inside the
+// Sums N values over a row's group of gw warps; warp is the one inside the
 // group. Every thread of the block takes part (groups of one warp need no
 // barrier). slot alternates between calls, so one barrier a call is enough.
-__device__ __forceinline__ float2 group_sum(float a, float b, int gw, int group, int warp, int lane, int slot) {
-    __shared__ float2 part[2][kNormThreads / 32];
-    a = warp_sum(a);
-    b = warp_sum(b);
-    if (gw == 1) return make_float2(a, b);
-    float2* p = part[slot] + group * gw;
-    if (lane == 0) p[warp] = make_float2(a, b);
-    __syncthreads();
-    float2 s = p[0];
-    for (int i = 1; i < gw; ++i) {
-        s.x += p[i].x;
-        s.y += p[i].y;
-    }
-    return s;
-}
-
-template <typename P>
-__device__ __forceinline__ void load_param(float (&x)[8], const void* p, int64_t c, int n, float none) {
-    if (!p) {
+template <int N>
+__device__ __forceinline__ void group_sum(float (&x)[N], int gw, int group, int warp, int lane, int slot) {
+    __shared__ float part[2][N][kWarps];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = none;
-        return;
+    for (int i = 0; i < N; ++i) x[i] = warp_sum(x[i]);
+    if (gw == 1) return;
+    if (lane == 0)
+#pragma unroll
+        for (int i = 0; i < N; ++i) part[slot][i][group * gw + warp] = x[i];
+    __syncthreads();
+    // every warp adds the group's parts, at most 16, in the same order
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        float s = (lane & 15) < gw ? part[slot][i][group * gw + (lane & 15)] : 0.0f;
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
+        x[i] = s;
     }
-    Raw<P> r;
-    load_granule(r, static_cast<const P*>(p), c, n);
-    widen(r, x);
 }
 
-// The n columns of granule g of h = residual + drop(x).
+// A parameter's granule, every row's again: it stays in the L1 cache, and held
+// in registers it would cost half the warps.
+template <bool kAligned, typename P>
+__device__ __forceinline__ Cols load_param_as(const void* p, int64_t c, int n) {
+    Raw<P> r;
+    if constexpr (kAligned) {
+        if (n) {
+            const uint4* q = reinterpret_cast<const uint4*>(static_cast<const P*>(p) + c);
+#pragma unroll
+            for (int v = 0; v < Raw<P>::kVec; ++v) put(r.w + 4 * v, ld_reuse(q + v));
+        }
+    } else {
+        load_granule(r, static_cast<const P*>(p), c, n);
+    }
+    return widened(r);
+}
+template <bool kAligned>
+__device__ __forceinline__ Cols load_param(const void* p, int dt, int64_t c, int n, float none) {
+    if (!p) return all(none);
+    return dt == FSDP_F32 ? load_param_as<kAligned, float>(p, c, n) : load_param_as<kAligned, uint16_t>(p, c, n);
+}
+
+// What h is made of, and what its gradient takes: a kernel's kMode holds
+// kResidual (a residual; a gradient past the norm) and kDrops as bits, or
+// leaves both to the call (kEither).
+constexpr int kResidual = 1, kDrops = 2, kEither = -1;
+template <int kMode>
+__device__ __forceinline__ bool has(int bit, bool given) {
+    return kMode == kEither ? given : (kMode & bit) != 0;
+}
+
+// Waits until all but the newest `left` groups of this thread's copies are in.
+__device__ __forceinline__ void async_wait_but(int left) {
+    if (left == 3)
+        async_wait<3>();
+    else if (left == 2)
+        async_wait<2>();
+    else if (left == 1)
+        async_wait<1>();
+    else
+        async_wait<0>();
+}
+
+// ------------------------------------------------------------------ forward
+
+template <int kMode, typename T>
+__device__ __forceinline__ Cols make_hidden(const Raw<T>& x, const Raw<T>& res, const NormArgs& a, int64_t row,
+                                            int64_t g) {
+    Cols h = has<kMode>(kResidual, a.res.data) ? widened(res) : all(0.0f);
+    if (has<kMode>(kDrops, a.mask.drops))
+        add_dropped(h, widened(x), a.mask, row, (uint32_t)g);
+    else
+        h = has<kMode>(kResidual, a.res.data) ? h + widened(x) : widened(x);
+    return h;
+}
+
+template <typename T, int V, bool kAligned, int kMode>
+__global__ void __launch_bounds__(V == 2 ? 256 : (V == 1 ? 128 : 512), V == 2 ? 4 : (V == 1 ? 8 : 1))
+    norm_kernel(NormArgs a, int gw, int depth) {
+    extern __shared__ uint4 ring[];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, group = w / gw, warp = w - group * gw;
+    const int groups = (blockDim.x >> 5) / gw, streams = has<kMode>(kResidual, a.res.data) ? 2 : 1;
+    const uint32_t rows = (uint32_t)a.rows, step = gridDim.x * groups;
+    const uint32_t xs = (uint32_t)a.x.stride * sizeof(T), rs = (uint32_t)a.res.stride * sizeof(T);
+    const uint32_t hs = (uint32_t)a.hidden.stride * sizeof(T), os = (uint32_t)a.out.stride * sizeof(T);
+    uint4* const mine = ring + (size_t)w * depth * streams * V * kSlot<kAligned, T>;
+    const int cols = (int)a.cols;
+    const float inv = 1.0f / (float)cols;
+
+    auto fetch = [&](uint32_t row, int slot) {
+        if (row < rows) {
+            uint4* s = mine + slot * streams * V * kSlot<kAligned, T>;
+            const T* x = row_at<const T>(a.x.data, row, xs);
+            const T* res = row_at<const T>(a.res.data, row, rs);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int c0 = (v * gw + warp) * kSpan;
+                span_fetch<kAligned>(s + v * kSlot<kAligned, T>, x, c0, cols, lane);
+                if (has<kMode>(kResidual, a.res.data)) span_fetch<kAligned>(s + (V + v) * kSlot<kAligned, T>, res, c0, cols, lane);
+            }
+        }
+        async_commit();
+    };
+
+    uint32_t row = blockIdx.x * groups + group;
+    for (int d = 0; d + 1 < depth; ++d) fetch(row + d * step, d);
+    int slot = 0;
+    // every group of a block goes round as often, for the barriers
+    for (uint32_t r0 = blockIdx.x * groups; r0 < rows; r0 += step, row += step) {
+        __syncwarp();  // the slot's last reads
+        fetch(row + (depth - 1) * step, slot == 0 ? depth - 1 : slot - 1);
+        async_wait_but(depth - 1);
+        __syncwarp();
+        const bool on = row < rows;
+        const T* x = row_at<const T>(a.x.data, row, xs);
+        const T* res = row_at<const T>(a.res.data, row, rs);
+        Cols h[V];
+        float2 s = both(0.0f);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int g = (v * gw + warp) * 32 + lane, c0 = (v * gw + warp) * kSpan;
+            const int n = on ? granule_cols(g, cols) : 0;
+            const uint4* from = mine + (slot * streams * V + v) * kSlot<kAligned, T>;
+            Raw<T> r, q;
+            span_read<kAligned>(r, from, x, c0, lane);
+            if (has<kMode>(kResidual, a.res.data)) span_read<kAligned>(q, from + V * kSlot<kAligned, T>, res, c0, lane);
+            h[v] = make_hidden<kMode>(r, q, a, row, g);
+            if (a.hidden.data) {
+                round_to(h[v], r);
+                store_cols<kAligned>(row_at<T>(a.hidden.data, row, hs) + g * kGran, r, n, lane);
+            }
+            if (!kAligned) cut(h[v], n);
+            if (!kAligned || n) sum_into(s, h[v]);
+        }
+        float sum[1] = {s.x + s.y};
+        group_sum(sum, gw, group, warp, lane, 0);
+        const float mean = sum[0] / (float)cols;  // equal values give their own; a product with 1 / cols may not
+        s = both(0.0f);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int n = on ? granule_cols((v * gw + warp) * 32 + lane, cols) : 0;
+            h[v] = h[v] + all(-mean);
+            if (!kAligned) cut(h[v], n);
+            if (!kAligned || n) dot_into(s, h[v], h[v]);
+        }
+        sum[0] = s.x + s.y;
+        group_sum(sum, gw, group, warp, lane, 1);
+        slot = slot + 1 == depth ? 0 : slot + 1;
+        if (!on) continue;
+        const float rstd = rsqrtf(__fmaf_rn(sum[0], inv, a.eps));
+        if (warp == 0 && lane == 0) {
+            if (a.mean) a.mean[row] = mean;
+            if (a.rstd) a.rstd[row] = rstd;
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int g = (v * gw + warp) * 32 + lane;
+            const int n = granule_cols(g, cols);
+            Raw<T> r;
+            round_to(fma(h[v] * all(rstd), load_param<kAligned>(a.weight, a.param_dt, g * kGran, n, 1.0f),
+                         load_param<kAligned>(a.bias, a.param_dt, g * kGran, n, 0.0f)),
+                     r);
+            store_cols<kAligned>(row_at<T>(a.out.data, row, os) + g * kGran, r, n, lane);
+        }
+    }
+}
+
+// The columns of granule g of h, straight from memory.
 template <typename T>
-__device__ __forceinline__ void load_hidden(float (&h)[8], const NormArgs& a, int64_t row, int64_t g, int n) {
+__device__ __forceinline__ Cols load_hidden(const NormArgs& a, int64_t row, int64_t g, int n) {
     Raw<T> r, q;
     load_granule(r, static_cast<const T*>(a.x.data) + row * a.x.stride, g * kGran, n);
     if (a.res.data) load_granule(q, static_cast<const T*>(a.res.data) + row * a.res.stride, g * kGran, n);
-    widen(r, h);
-    if (a.mask.limit < 65536) drop(h, a.mask, row, (uint32_t)g);
-    if (a.res.data) {
-        float y[8];
-        widen(q, y);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) h[e] += y[e];
-    }
+    Cols h = make_hidden<kEither>(r, q, a, row, g);
+    cut(h, n);
+    return h;
 }
 
-template <typename T, typename P>
-__device__ __forceinline__ void store_norm(const NormArgs& a, float (&h)[8], float mean, float rstd, int64_t row,
-                                           int64_t g, int n, int lane) {
-    float w[8], b[8];
-    load_param<P>(w, a.weight, g * kGran, n, 1.0f);
-    load_param<P>(b, a.bias, g * kGran, n, 0.0f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) h[e] = __fmaf_rn((h[e] - mean) * rstd, w[e], b[e]);
-    Raw<T> r;
-    narrow(h, r);
-    store_span(static_cast<T*>(a.out.data) + row * a.out.stride + g * kGran, r, n, lane);
-}
-
-// Rows in registers: V granules a thread, gw warps a row.
-template <typename T, typename P, int V>
-__global__ void __launch_bounds__(kNormThreads) norm_kernel(NormArgs a, int gw) {
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, group = w / gw, warp = w % gw;
-    const int groups = (blockDim.x >> 5) / gw;
-    const int64_t row = (int64_t)blockIdx.x * groups + group;
-    const bool on = row < a.rows;
-    float h[V][8];
-    float s = 0.0f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int64_t g = (v * gw + warp) * 32 + lane;
-        const int n = on ? granule_cols(g, a.cols) : 0;
-        if (on) load_hidden<T>(h[v], a, row, g, n);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s += e < n ? h[v][e] : 0.0f;
-    }
-    const float mean = group_sum(s, 0.0f, gw, group, warp, lane, 0).x / (float)a.cols;
-    s = 0.0f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int n = on ? granule_cols((v * gw + warp) * 32 + lane, a.cols) : 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s = e < n ? __fmaf_rn(h[v][e] - mean, h[v][e] - mean, s) : s;
-    }
-    const float var = group_sum(s, 0.0f, gw, group, warp, lane, 1).x / (float)a.cols;
-    if (!on) return;
-    const float rstd = 1.0f / sqrtf(var + a.eps);
-    if (warp == 0 && lane == 0) {
-        if (a.mean) a.mean[row] = mean;
-        if (a.rstd) a.rstd[row] = rstd;
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int64_t g = (v * gw + warp) * 32 + lane;
-        const int n = granule_cols(g, a.cols);
-        if (a.hidden.data) {
-            Raw<T> r;
-            narrow(h[v], r);
-            store_span(static_cast<T*>(a.hidden.data) + row * a.hidden.stride + g * kGran, r, n, lane);
-        }
-        store_norm<T, P>(a, h[v], mean, rstd, row, g, n, lane);
-    }
-}
-
-// Rows too wide for registers: a block reads the row's inputs once for each
-// of the mean, the variance and the output.
-template <typename T, typename P>
-__global__ void __launch_bounds__(kNormThreads) norm_wide_kernel(NormArgs a) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gw = kNormThreads / 32;
+// Rows too wide for registers, or too far apart for 32-bit strides: a block
+// reads the row's inputs once for each of the mean, the variance and the
+// output.
+template <typename T>
+__global__ void __launch_bounds__(kWideThreads) norm_wide_kernel(NormArgs a) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gw = kWideThreads / 32;
     const int64_t row = blockIdx.x, end = (a.cols + kSpan - 1) / kSpan * 32;
-    float h[8], s = 0.0f;
-    for (int64_t g = threadIdx.x; g < end; g += kNormThreads) {
-        const int n = granule_cols(g, a.cols);
-        load_hidden<T>(h, a, row, g, n);
-        float t = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) t += e < n ? h[e] : 0.0f;
-        s += t;
+    float sum[1] = {0.0f};
+    for (int64_t g = threadIdx.x; g < end; g += kWideThreads) {
+        float2 s = both(0.0f);
+        sum_into(s, load_hidden<T>(a, row, g, granule_cols(g, a.cols)));
+        sum[0] += s.x + s.y;
     }
-    const float mean = group_sum(s, 0.0f, gw, 0, warp, lane, 0).x / (float)a.cols;
-    s = 0.0f;
-    for (int64_t g = threadIdx.x; g < end; g += kNormThreads) {
+    group_sum(sum, gw, 0, warp, lane, 0);
+    const float mean = sum[0] / (float)a.cols;
+    sum[0] = 0.0f;
+    for (int64_t g = threadIdx.x; g < end; g += kWideThreads) {
         const int n = granule_cols(g, a.cols);
-        load_hidden<T>(h, a, row, g, n);
-        float t = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) t = e < n ? __fmaf_rn(h[e] - mean, h[e] - mean, t) : t;
-        s += t;
+        Cols d = load_hidden<T>(a, row, g, n) + all(-mean);
+        cut(d, n);
+        float2 s = both(0.0f);
+        dot_into(s, d, d);
+        sum[0] += s.x + s.y;
     }
-    const float var = group_sum(s, 0.0f, gw, 0, warp, lane, 1).x / (float)a.cols;
-    const float rstd = 1.0f / sqrtf(var + a.eps);
+    group_sum(sum, gw, 0, warp, lane, 1);
+    const float rstd = rsqrtf(sum[0] / (float)a.cols + a.eps);
     if (threadIdx.x == 0) {
         if (a.mean) a.mean[row] = mean;
         if (a.rstd) a.rstd[row] = rstd;
     }
-    for (int64_t g = threadIdx.x; g < end; g += kNormThreads) {
+    for (int64_t g = threadIdx.x; g < end; g += kWideThreads) {
         const int n = granule_cols(g, a.cols);
-        load_hidden<T>(h, a, row, g, n);
+        const Cols h = load_hidden<T>(a, row, g, n);
+        Raw<T> r;
         if (a.hidden.data) {
-            Raw<T> r;
-            narrow(h, r);
+            round_to(h, r);
             store_span(static_cast<T*>(a.hidden.data) + row * a.hidden.stride + g * kGran, r, n, lane);
         }
-        store_norm<T, P>(a, h, mean, rstd, row, g, n, lane);
+        round_to(fma((h + all(-mean)) * all(rstd), load_param<false>(a.weight, a.param_dt, g * kGran, n, 1.0f),
+                     load_param<false>(a.bias, a.param_dt, g * kGran, n, 0.0f)),
+                 r);
+        store_span(static_cast<T*>(a.out.data) + row * a.out.stride + g * kGran, r, n, lane);
     }
-}
-
-template <typename T, typename P>
-cudaError_t norm(const NormArgs& a, cudaStream_t s) {
-    const int64_t grans = (a.cols + kGran - 1) / kGran;
-    if (a.cols > kNormCols) {
-        norm_wide_kernel<T, P><<<(unsigned)a.rows, kNormThreads, 0, s>>>(a);
-    } else {
-        const int v = grans <= 32 * 4 ? 1 : (grans <= 32 * 16 ? 2 : 4);
-        const int gw = (int)((grans + 32 * v - 1) / (32 * v));
-        const int groups = gw >= 4 ? 1 : 4 / gw;
-        const unsigned grid = (unsigned)((a.rows + groups - 1) / groups);
-        const int block = 32 * gw * groups;
-        if (v == 1)
-            norm_kernel<T, P, 1><<<grid, block, 0, s>>>(a, gw);
-        else if (v == 2)
-            norm_kernel<T, P, 2><<<grid, block, 0, s>>>(a, gw);
-        else
-            norm_kernel<T, P, 4><<<grid, block, 0, s>>>(a, gw);
-    }
-    count_launch();
-    return cudaGetLastError();
 }
 
 // ----------------------------------------------------------------- gradient
 
-// What a row's gradient needs at one granule: the gradients and u.
-template <typename T, typename P>
+// grad_hidden's share and the dropout behind it, rounded and stored. (What t
+// holds past the row's end is not stored.)
+template <bool kAligned, int kMode, typename T>
+__device__ __forceinline__ void store_grad(const NormGradArgs& a, const Cols& t, int64_t row, int64_t g, int n, int lane,
+                                           T* grad_res, T* grad_x) {
+    Raw<T> r;
+    round_to(t, r);
+    if (a.grad_res.data) store_cols<kAligned>(grad_res + g * kGran, r, n, lane);
+    if (has<kMode>(kDrops, a.mask.drops)) {
+        Cols y = all(0.0f);
+        add_dropped(y, t, a.mask, row, (uint32_t)g);
+        round_to(y, r);
+    }
+    store_cols<kAligned>(grad_x + g * kGran, r, n, lane);
+}
+
+// parts[block][0 weight, 1 bias][stride]: the sums of a block's rows.
+template <typename T, int V, bool kAligned, int kMode>
+__global__ void __launch_bounds__(V == 1 ? 128 : 512, V == 1 ? 8 : 1)
+    norm_grad_kernel(NormGradArgs a, int gw, int depth, int64_t stride) {
+    extern __shared__ uint4 ring[];
+    allow_next();
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, group = w / gw, warp = w - group * gw;
+    const int groups = (blockDim.x >> 5) / gw, streams = has<kMode>(kResidual, a.grad_hidden.data) ? 3 : 2;
+    const uint32_t rows = (uint32_t)a.rows, step = gridDim.x * groups;
+    const uint32_t gs = (uint32_t)a.grad.stride * sizeof(T), hs = (uint32_t)a.hidden.stride * sizeof(T);
+    const uint32_t as = (uint32_t)a.grad_hidden.stride * sizeof(T);
+    const uint32_t rs = (uint32_t)a.grad_res.stride * sizeof(T), xs = (uint32_t)a.grad_x.stride * sizeof(T);
+    constexpr int kOne = kSlot<kAligned, T>;
+    uint4* const mine = ring + (size_t)w * depth * streams * V * kOne;
+    const int cols = (int)a.cols;
+    const float inv = 1.0f / (float)cols;
+
+    auto fetch = [&](uint32_t row, int slot) {
+        if (row < rows) {
+            uint4* s = mine + slot * streams * V * kOne;
+            const T* dy = row_at<const T>(a.grad.data, row, gs);
+            const T* h = row_at<const T>(a.hidden.data, row, hs);
+            const T* past = row_at<const T>(a.grad_hidden.data, row, as);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int c0 = (v * gw + warp) * kSpan;
+                span_fetch<kAligned>(s + v * kOne, dy, c0, cols, lane);
+                span_fetch<kAligned>(s + (V + v) * kOne, h, c0, cols, lane);
+                if (has<kMode>(kResidual, a.grad_hidden.data)) span_fetch<kAligned>(s + (2 * V + v) * kOne, past, c0, cols, lane);
+            }
+        }
+        async_commit();
+    };
+
+    Cols dw[V], db[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) dw[v] = db[v] = all(0.0f);
+    uint32_t row = blockIdx.x * groups + group;
+    for (int d = 0; d + 1 < depth; ++d) fetch(row + d * step, d);
+    // a row's mean and rstd are loaded a row ahead
+    float next_mean = row < rows ? __ldg(a.mean + row) : 0.0f, next_rstd = row < rows ? __ldg(a.rstd + row) : 0.0f;
+    int slot = 0, side = 0;
+    for (uint32_t r0 = blockIdx.x * groups; r0 < rows; r0 += step, row += step) {
+        __syncwarp();
+        fetch(row + (depth - 1) * step, slot == 0 ? depth - 1 : slot - 1);
+        const float mean = next_mean, rstd = next_rstd;
+        if (row + step < rows) {
+            next_mean = __ldg(a.mean + row + step);
+            next_rstd = __ldg(a.rstd + row + step);
+        }
+        async_wait_but(depth - 1);
+        __syncwarp();
+        const bool on = row < rows;
+        const T* dyp = row_at<const T>(a.grad.data, row, gs);
+        const T* hp = row_at<const T>(a.hidden.data, row, hs);
+        const T* past = row_at<const T>(a.grad_hidden.data, row, as);
+        const uint4* const from = mine + slot * streams * V * kOne;
+        Cols u[V], gr[V];
+        float2 s1 = both(0.0f), s2 = both(0.0f);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int g = (v * gw + warp) * 32 + lane, c0 = (v * gw + warp) * kSpan;
+            const int n = on ? granule_cols(g, cols) : 0;
+            Raw<T> r, q;
+            span_read<kAligned>(r, from + v * kOne, dyp, c0, lane);
+            span_read<kAligned>(q, from + (V + v) * kOne, hp, c0, lane);
+            Cols dy = widened(r);
+            u[v] = (widened(q) + all(-mean)) * all(rstd);
+            if (!kAligned) {
+                cut(dy, n);
+                cut(u[v], n);
+            }
+            if (!kAligned || n) {
+                gr[v] = dy * load_param<kAligned>(a.weight, a.param_dt, g * kGran, n, 1.0f);
+                db[v] = db[v] + dy;
+                dw[v] = fma(dy, u[v], dw[v]);
+                sum_into(s1, gr[v]);
+                dot_into(s2, gr[v], u[v]);
+            }
+        }
+        float c[2] = {s1.x + s1.y, s2.x + s2.y};
+        group_sum(c, gw, group, warp, lane, side);
+        side ^= 1;
+        if (on) {
+            const Cols k0 = all(rstd), k1 = all(-(c[0] * inv)), k2 = all(-(c[1] * inv));
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int g = (v * gw + warp) * 32 + lane, c0 = (v * gw + warp) * kSpan;
+                const int n = granule_cols(g, cols);
+                Cols t = fma(u[v], k2, gr[v] + k1);
+                if (has<kMode>(kResidual, a.grad_hidden.data)) {
+                    Raw<T> r;
+                    span_read<kAligned>(r, from + (2 * V + v) * kOne, past, c0, lane);
+                    t = fma(t, k0, widened(r));
+                } else {
+                    t = t * k0;
+                }
+                store_grad<kAligned, kMode>(a, t, row, g, n, lane, row_at<T>(a.grad_res.data, row, rs), row_at<T>(a.grad_x.data, row, xs));
+            }
+        }
+        slot = slot + 1 == depth ? 0 : slot + 1;
+    }
+    // the block's groups, added in turn
+    float4* const box = reinterpret_cast<float4*>(ring);
+    for (int k = 1; k < groups; ++k) {
+        __syncthreads();
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float4* q = box + ((v * 4 + i) * gw + warp) * 32 + lane;
+                if (group == k) *q = make_float4(dw[v].p[i].x, dw[v].p[i].y, db[v].p[i].x, db[v].p[i].y);
+            }
+        __syncthreads();
+        if (group == 0)
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 q = box[((v * 4 + i) * gw + warp) * 32 + lane];
+                    dw[v].p[i] = __fadd2_rn(dw[v].p[i], make_float2(q.x, q.y));
+                    db[v].p[i] = __fadd2_rn(db[v].p[i], make_float2(q.z, q.w));
+                }
+    }
+    if (group != 0) return;
+    float* const p = a.work + (int64_t)blockIdx.x * 2 * stride;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int c = ((v * gw + warp) * 32 + lane) * kGran;
+        if (c >= cols) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            *reinterpret_cast<float2*>(p + c + 2 * i) = dw[v].p[i];
+            *reinterpret_cast<float2*>(p + stride + c + 2 * i) = db[v].p[i];
+        }
+    }
+}
+
+// What a row's gradient needs at one granule, straight from memory.
+template <typename T>
 __device__ __forceinline__ void load_grad(const NormGradArgs& a, float mean, float rstd, int64_t row, int64_t g, int n,
-                                          float (&dy)[8], float (&u)[8], float (&gw)[8]) {
+                                          Cols& dy, Cols& u, Cols& gr) {
     Raw<T> r, q;
     load_granule(r, static_cast<const T*>(a.grad.data) + row * a.grad.stride, g * kGran, n);
     load_granule(q, static_cast<const T*>(a.hidden.data) + row * a.hidden.stride, g * kGran, n);
-    float w[8];
-    load_param<P>(w, a.weight, g * kGran, n, 1.0f);
-    widen(r, dy);
-    widen(q, u);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        u[e] = e < n ? (u[e] - mean) * rstd : 0.0f;
-        gw[e] = dy[e] * w[e];
-    }
+    dy = widened(r);
+    u = (widened(q) + all(-mean)) * all(rstd);
+    cut(u, n);
+    gr = dy * load_param<false>(a.weight, a.param_dt, g * kGran, n, 1.0f);
 }
 
+// Rows too wide for registers, or too far apart for 32-bit strides: the rows'
+// gradients, a block each ...
 template <typename T>
-__device__ __forceinline__ void store_grad(const NormGradArgs& a, float rstd, float c1, float c2, int64_t row,
-                                           int64_t g, int n, int lane, const float (&u)[8], const float (&gw)[8]) {
-    float t[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) t[e] = rstd * (gw[e] - c1 - u[e] * c2);
-    Raw<T> r;
-    if (a.grad_hidden.data) {
-        float y[8];
-        load_granule(r, static_cast<const T*>(a.grad_hidden.data) + row * a.grad_hidden.stride, g * kGran, n);
-        widen(r, y);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) t[e] += y[e];
-    }
-    if (a.grad_res.data) {
-        narrow(t, r);
-        store_span(static_cast<T*>(a.grad_res.data) + row * a.grad_res.stride + g * kGran, r, n, lane);
-    }
-    if (a.mask.limit < 65536) drop(t, a.mask, row, (uint32_t)g);
-    narrow(t, r);
-    store_span(static_cast<T*>(a.grad_x.data) + row * a.grad_x.stride + g * kGran, r, n, lane);
-}
-
-// parts[part][0 weight, 1 bias][stride]: the sums of one group's rows.
-template <typename T, typename P, int V>
-__global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(NormGradArgs a, int gw, int64_t stride) {
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, group = w / gw, warp = w % gw;
-    const int groups = (blockDim.x >> 5) / gw;
-    float dw[V][8] = {}, db[V][8] = {};
-    int slot = 0;
-    for (int64_t r0 = (int64_t)blockIdx.x * groups; r0 < a.rows; r0 += (int64_t)gridDim.x * groups) {
-        const int64_t row = r0 + group;
-        const bool on = row < a.rows;
-        const float mean = on ? __ldg(a.mean + row) : 0.0f, rstd = on ? __ldg(a.rstd + row) : 0.0f;
-        float u[V][8], g1[V][8];
-        float s1 = 0.0f, s2 = 0.0f;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int64_t g = (v * gw + warp) * 32 + lane;
-            const int n = on ? granule_cols(g, a.cols) : 0;
-            float dy[8];
-            if (on) {
-                load_grad<T, P>(a, mean, rstd, row, g, n, dy, u[v], g1[v]);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    db[v][e] += dy[e];
-                    dw[v][e] = __fmaf_rn(dy[e], u[v][e], dw[v][e]);
-                    if (e < n) {
-                        s1 += g1[v][e];
-                        s2 = __fmaf_rn(g1[v][e], u[v][e], s2);
-                    }
-                }
-            }
-        }
-        const float2 c = group_sum(s1, s2, gw, group, warp, lane, slot);
-        slot ^= 1;
-        if (!on) continue;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int64_t g = (v * gw + warp) * 32 + lane;
-            store_grad<T>(a, rstd, c.x / (float)a.cols, c.y / (float)a.cols, row, g, granule_cols(g, a.cols), lane,
-                          u[v], g1[v]);
-        }
-    }
-    float* p = a.work + ((int64_t)blockIdx.x * groups + group) * 2 * stride;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int64_t c = ((v * gw + warp) * 32 + lane) * (int64_t)kGran;
-        if (c >= a.cols) continue;
-        float4* q = reinterpret_cast<float4*>(p + c);
-        q[0] = make_float4(dw[v][0], dw[v][1], dw[v][2], dw[v][3]);
-        q[1] = make_float4(dw[v][4], dw[v][5], dw[v][6], dw[v][7]);
-        q = reinterpret_cast<float4*>(p + stride + c);
-        q[0] = make_float4(db[v][0], db[v][1], db[v][2], db[v][3]);
-        q[1] = make_float4(db[v][4], db[v][5], db[v][6], db[v][7]);
-    }
-}
-
-// Rows too wide for registers: the rows' gradients, a block each ...
-template <typename T, typename P>
-__global__ void __launch_bounds__(kNormThreads) norm_grad_wide_kernel(NormGradArgs a) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gw = kNormThreads / 32;
+__global__ void __launch_bounds__(kWideThreads) norm_grad_wide_kernel(NormGradArgs a) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gw = kWideThreads / 32;
     const int64_t row = blockIdx.x, end = (a.cols + kSpan - 1) / kSpan * 32;
     const float mean = __ldg(a.mean + row), rstd = __ldg(a.rstd + row);
-    float dy[8], u[8], g1[8], s1 = 0.0f, s2 = 0.0f;
-    for (int64_t g = threadIdx.x; g < end; g += kNormThreads) {
-        const int n = granule_cols(g, a.cols);
-        load_grad<T, P>(a, mean, rstd, row, g, n, dy, u, g1);
-        float t1 = 0.0f, t2 = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (e < n) {
-                t1 += g1[e];
-                t2 = __fmaf_rn(g1[e], u[e], t2);
-            }
-        s1 += t1;
-        s2 += t2;
+    Cols dy, u, gr;
+    float c[2] = {0.0f, 0.0f};
+    for (int64_t g = threadIdx.x; g < end; g += kWideThreads) {
+        load_grad<T>(a, mean, rstd, row, g, granule_cols(g, a.cols), dy, u, gr);
+        float2 s1 = both(0.0f), s2 = both(0.0f);
+        sum_into(s1, gr);
+        dot_into(s2, gr, u);
+        c[0] += s1.x + s1.y;
+        c[1] += s2.x + s2.y;
     }
-    const float2 c = group_sum(s1, s2, gw, 0, warp, lane, 0);
-    for (int64_t g = threadIdx.x; g < end; g += kNormThreads) {
+    group_sum(c, gw, 0, warp, lane, 0);
+    const Cols k1 = all(-(c[0] / (float)a.cols)), k2 = all(-(c[1] / (float)a.cols));
+    for (int64_t g = threadIdx.x; g < end; g += kWideThreads) {
         const int n = granule_cols(g, a.cols);
-        load_grad<T, P>(a, mean, rstd, row, g, n, dy, u, g1);
-        store_grad<T>(a, rstd, c.x / (float)a.cols, c.y / (float)a.cols, row, g, n, lane, u, g1);
+        load_grad<T>(a, mean, rstd, row, g, n, dy, u, gr);
+        Cols t = fma(u, k2, gr + k1) * all(rstd);
+        if (a.grad_hidden.data) {
+            Raw<T> r;
+            load_granule(r, static_cast<const T*>(a.grad_hidden.data) + row * a.grad_hidden.stride, g * kGran, n);
+            t = t + widened(r);
+        }
+        store_grad<false, kEither>(a, t, row, g, n, lane, static_cast<T*>(a.grad_res.data) + row * a.grad_res.stride,
+                                   static_cast<T*>(a.grad_x.data) + row * a.grad_x.stride);
     }
 }
 // ... and the weight's and bias's sums, a warp for a span of columns and a
 // share of the rows.
-template <typename T, typename P>
+template <typename T>
 __global__ void __launch_bounds__(256) norm_param_kernel(NormGradArgs a, int64_t stride, int parts) {
     const int lane = threadIdx.x & 31, part = blockIdx.y * 8 + (threadIdx.x >> 5);
     const int64_t g = (int64_t)blockIdx.x * 32 + lane, c = g * kGran;
     const int n = granule_cols(g, a.cols);
     if (part >= parts || n == 0) return;
-    float dw[8] = {}, db[8] = {};
+    Cols dw = all(0.0f), db = all(0.0f);
     for (int64_t row = part; row < a.rows; row += parts) {
-        float dy[8], u[8], g1[8];
-        load_grad<T, P>(a, __ldg(a.mean + row), __ldg(a.rstd + row), row, g, n, dy, u, g1);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            db[e] += dy[e];
-            dw[e] = __fmaf_rn(dy[e], u[e], dw[e]);
-        }
+        Cols dy, u, gr;
+        load_grad<T>(a, __ldg(a.mean + row), __ldg(a.rstd + row), row, g, n, dy, u, gr);
+        db = db + dy;
+        dw = fma(dy, u, dw);
     }
     float* p = a.work + (int64_t)part * 2 * stride + c;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        p[e] = dw[e];
-        p[stride + e] = db[e];
+        p[e] = dw.get(e);
+        p[stride + e] = db.get(e);
     }
 }
 
 // Adds the parts' sums, 32 columns a block, a share of the parts for each of
-// its 8 warps: blockIdx.y 0 the weight's, 1 the bias's.
+// its warps: blockIdx.y 0 the weight's, 1 the bias's.
+constexpr int kJoinWarps = 16;
 template <typename G>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(32 * kJoinWarps)
     norm_join_kernel(const float* work, int64_t stride, int parts, int64_t cols, int accumulate, G* gw, G* gb) {
-    __shared__ float sums[8][32];
+    __shared__ float sums[kJoinWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;
     G* out = blockIdx.y ? gb : gw;
+    wait_for_previous();
     if (!out) return;
     float s = 0.0f;
-    if (c < cols)
-        for (int p = parts * warp / 8; p < parts * (warp + 1) / 8; ++p) s += __ldcg(work + (2 * (int64_t)p + blockIdx.y) * stride + c);
+    if (c < cols) {
+        const float* from = work + blockIdx.y * stride + c;
+#pragma unroll 8
+        for (int p = parts * warp / kJoinWarps; p < parts * (warp + 1) / kJoinWarps; ++p) s += __ldcg(from + 2 * (int64_t)p * stride);
+    }
     sums[warp][lane] = s;
     __syncthreads();
     if (warp != 0 || c >= cols) return;
     s = 0.0f;
-    for (int q = 0; q < 8; ++q) s += sums[q][lane];
+#pragma unroll
+    for (int q = 0; q < kJoinWarps; ++q) s += sums[q][lane];
     if (accumulate) s += load_f32(out, c);
     store_f32(out, c, s);
 }
 
-struct NormGradPlan {
-    bool wide;
-    int v, gw, groups, grid, parts;
-    int64_t stride;
+// ----------------------------------------------------------------- launches
+
+// Whether the rows' strides and numbers fit the 32-bit arithmetic of the
+// kernels that keep rows in registers.
+bool fits_32(const Mat& m, int es) { return m.stride < ((int64_t)1 << 32) / es; }
+
+// What the blocks of an SM may take of shared memory together: the rest of
+// its 256 KB is the L1 cache, where the parameters stay.
+constexpr int64_t kSmemPerSm = 132 * 1024, kSmemMost = 200 * 1024;
+
+// How a kernel is launched on rows of these columns: V granules a thread, gw
+// warps a row, groups of them in a block, blocks of an SM, and the rows that
+// its shared memory holds.
+struct Shape {
+    int v, gw, groups, per_sm, grid, depth;
+    int64_t smem;
 };
 
-NormGradPlan grad_plan(int64_t rows, int64_t cols) {
-    NormGradPlan p;
+Shape norm_shape(int64_t rows, int64_t cols, int streams, int slot_bytes) {
+    Shape f;
     const int64_t grans = (cols + kGran - 1) / kGran;
-    p.stride = grans * kGran;
-    p.wide = cols > kNormCols;
-    if (p.wide) {
-        p.v = p.gw = p.groups = p.grid = 0;
-        p.parts = (int)(rows < 256 ? rows : 256);
-        return p;
-    }
-    p.v = grans <= 32 * 8 ? 1 : (grans <= 32 * 16 ? 2 : 4);
-    p.gw = (int)((grans + 32 * p.v - 1) / (32 * p.v));
-    p.groups = p.gw >= 4 ? 1 : 4 / p.gw;
-    const int64_t blocks = (rows + p.groups - 1) / p.groups;
-    p.grid = (int)(blocks < 304 ? blocks : 304);
-    p.parts = p.grid * p.groups;
-    return p;
+    // few warps a row make its two sums cheap; 4 granules a thread and two
+    // blocks of 8 warps ran 8192 columns in 182 us, 2 granules and 16 warps
+    // in 202 (16384 rows of bf16, dropout and residual)
+    f.v = grans <= 32 * 4 ? 1 : (grans <= 32 * 16 ? 2 : 4);
+    f.gw = (int)((grans + 32 * f.v - 1) / (32 * f.v));
+    f.groups = f.gw >= 4 ? 1 : 4 / f.gw;
+    const int block = 32 * f.gw * f.groups;
+    f.per_sm = f.v <= 2 ? 1024 / block : (512 / block);
+    const int64_t need = (rows + f.groups - 1) / f.groups;
+    const int64_t most = (int64_t)sm_count() * f.per_sm;
+    f.grid = (int)(need < most ? need : most);
+    const int64_t stage = (int64_t)f.gw * f.groups * f.v * slot_bytes * streams;
+    int64_t depth = kSmemPerSm / f.per_sm / stage;
+    if (depth > 4) depth = 4;
+    if (depth > (need + f.grid - 1) / f.grid) depth = (need + f.grid - 1) / f.grid;
+    f.depth = (int)(depth > 1 ? depth : 1);
+    f.smem = stage * f.depth;
+    return f;
 }
 
-template <typename T, typename P>
-cudaError_t norm_grad_rows(const NormGradArgs& a, const NormGradPlan& p, cudaStream_t s) {
-    if (p.wide) {
-        norm_grad_wide_kernel<T, P><<<(unsigned)a.rows, kNormThreads, 0, s>>>(a);
-        count_launch();
-        const dim3 grid((unsigned)((a.cols + kSpan - 1) / kSpan), (unsigned)((p.parts + 7) / 8));
-        norm_param_kernel<T, P><<<grid, 256, 0, s>>>(a, p.stride, p.parts);
-    } else if (p.v == 1) {
-        norm_grad_kernel<T, P, 1><<<p.grid, 32 * p.gw * p.groups, 0, s>>>(a, p.gw, p.stride);
-    } else if (p.v == 2) {
-        norm_grad_kernel<T, P, 2><<<p.grid, 32 * p.gw * p.groups, 0, s>>>(a, p.gw, p.stride);
-    } else {
-        norm_grad_kernel<T, P, 4><<<p.grid, 32 * p.gw * p.groups, 0, s>>>(a, p.gw, p.stride);
-    }
-    count_launch();
+template <typename T, int V, bool kAligned, int kMode>
+cudaError_t norm_rows(const NormArgs& a, const Shape& f, cudaStream_t s) {
+    auto kernel = norm_kernel<T, V, kAligned, kMode>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)f.smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)f.grid, 32 * f.gw * f.groups, f.smem, s>>>(a, f.gw, f.depth);
     return cudaGetLastError();
+}
+template <typename T, bool kAligned, int kMode>
+cudaError_t norm_v(const NormArgs& a, const Shape& f, cudaStream_t s) {
+    return f.v == 1 ? norm_rows<T, 1, kAligned, kMode>(a, f, s)
+           : f.v == 2 ? norm_rows<T, 2, kAligned, kMode>(a, f, s) : norm_rows<T, 4, kAligned, kMode>(a, f, s);
+}
+
+template <typename T>
+cudaError_t norm(const NormArgs& a, cudaStream_t s) {
+    const int es = (int)sizeof(T);
+    if (a.cols > kNormCols || !fits_32(a.x, es) || !fits_32(a.res, es) || !fits_32(a.hidden, es) || !fits_32(a.out, es)) {
+        norm_wide_kernel<T><<<(unsigned)a.rows, kWideThreads, 0, s>>>(a);
+        return cudaGetLastError();
+    }
+    const bool aligned = a.cols % kGran == 0 && on_grid(a.x, es) && on_grid(a.res, es) && on_grid(a.hidden, es) &&
+                         on_grid(a.out, es) && on_grid(Mat{const_cast<void*>(a.weight), 0}, es) &&
+                         on_grid(Mat{const_cast<void*>(a.bias), 0}, es);
+    const int mode = (a.res.data ? kResidual : 0) | (a.mask.drops ? kDrops : 0);
+    const Shape f = norm_shape(a.rows, a.cols, a.res.data ? 2 : 1, 16 * (aligned ? kSlot<true, T> : kSlot<false, T>));
+    if (!aligned) return norm_v<T, false, kEither>(a, f, s);
+    switch (mode) {
+        case 0: return norm_v<T, true, 0>(a, f, s);
+        case kResidual: return norm_v<T, true, kResidual>(a, f, s);
+        case kDrops: return norm_v<T, true, kDrops>(a, f, s);
+        default: return norm_v<T, true, kResidual | kDrops>(a, f, s);
+    }
+}
+
+Shape grad_shape(int64_t rows, int64_t cols, int streams, int slot_bytes) {
+    Shape f;
+    const int64_t grans = (cols + kGran - 1) / kGran;
+    f.v = grans <= 32 * 4 ? 1 : (grans <= 32 * 32 ? 2 : 4);
+    f.gw = (int)((grans + 32 * f.v - 1) / (32 * f.v));
+    f.groups = f.gw >= 4 ? 1 : 4 / f.gw;
+    const int block = 32 * f.gw * f.groups;
+    f.per_sm = (f.v == 1 ? 1024 : 512) / block;
+    if (f.per_sm < 1) f.per_sm = 1;
+    const int64_t need = (rows + f.groups - 1) / f.groups;
+    const int64_t most = (int64_t)sm_count() * f.per_sm;
+    f.grid = (int)(need < most ? need : most);
+    const int64_t stage = (int64_t)f.gw * f.groups * f.v * slot_bytes * streams;
+    int64_t depth = kSmemMost / f.per_sm / stage;
+    if (depth > 4) depth = 4;
+    if (depth > (need + f.grid - 1) / f.grid) depth = (need + f.grid - 1) / f.grid;
+    f.depth = (int)(depth > 1 ? depth : 1);
+    f.smem = stage * f.depth;
+    const int64_t box = f.groups > 1 ? (int64_t)f.gw * f.v * 2048 : 0;  // where the groups meet
+    if (f.smem < box) f.smem = box;
+    return f;
+}
+
+template <typename T, int V, bool kAligned, int kMode>
+cudaError_t grad_rows(const NormGradArgs& a, const Shape& f, int64_t stride, cudaStream_t s) {
+    auto kernel = norm_grad_kernel<T, V, kAligned, kMode>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)f.smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)f.grid, 32 * f.gw * f.groups, f.smem, s>>>(a, f.gw, f.depth, stride);
+    return cudaGetLastError();
+}
+template <typename T, bool kAligned, int kMode>
+cudaError_t grad_v(const NormGradArgs& a, const Shape& f, int64_t stride, cudaStream_t s) {
+    return f.v == 1 ? grad_rows<T, 1, kAligned, kMode>(a, f, stride, s)
+           : f.v == 2 ? grad_rows<T, 2, kAligned, kMode>(a, f, stride, s) : grad_rows<T, 4, kAligned, kMode>(a, f, stride, s);
+}
+
+constexpr int kWideParts = 256;
+int64_t grad_stride(int64_t cols) { return (cols + kGran - 1) / kGran * kGran; }
+
+// The rows' gradients and the parts' sums; *parts is how many there are.
+template <typename T>
+cudaError_t norm_grad(const NormGradArgs& a, int* parts, cudaStream_t s) {
+    const int es = (int)sizeof(T);
+    const int64_t stride = grad_stride(a.cols);
+    if (a.cols > kNormCols || !fits_32(a.grad, es) || !fits_32(a.hidden, es) || !fits_32(a.grad_hidden, es) ||
+        !fits_32(a.grad_res, es) || !fits_32(a.grad_x, es)) {
+        norm_grad_wide_kernel<T><<<(unsigned)a.rows, kWideThreads, 0, s>>>(a);
+        count_launch();
+        *parts = (int)(a.rows < kWideParts ? a.rows : kWideParts);
+        norm_param_kernel<T><<<dim3((unsigned)((a.cols + kSpan - 1) / kSpan), (unsigned)((*parts + 7) / 8)), 256, 0, s>>>(a, stride, *parts);
+        count_launch();
+        return cudaGetLastError();
+    }
+    const bool aligned = a.cols % kGran == 0 && on_grid(a.grad, es) && on_grid(a.hidden, es) && on_grid(a.grad_hidden, es) &&
+                         on_grid(a.grad_res, es) && on_grid(a.grad_x, es) && on_grid(Mat{const_cast<void*>(a.weight), 0}, es);
+    const int mode = (a.grad_hidden.data ? kResidual : 0) | (a.mask.drops ? kDrops : 0);
+    const Shape f = grad_shape(a.rows, a.cols, a.grad_hidden.data ? 3 : 2, 16 * (aligned ? kSlot<true, T> : kSlot<false, T>));
+    *parts = f.grid;
+    count_launch();
+    if (!aligned) return grad_v<T, false, kEither>(a, f, stride, s);
+    switch (mode) {
+        case 0: return grad_v<T, true, 0>(a, f, stride, s);
+        case kResidual: return grad_v<T, true, kResidual>(a, f, stride, s);
+        case kDrops: return grad_v<T, true, kDrops>(a, f, stride, s);
+        default: return grad_v<T, true, kResidual | kDrops>(a, f, stride, s);
+    }
 }
 
 }  // namespace
 
 size_t norm_grad_bytes(int64_t rows, int64_t cols) {
     if (rows == 0 || cols == 0) return 0;
-    const NormGradPlan p = grad_plan(rows, cols);
-    return (size_t)p.parts * 2 * p.stride * 4;
+    // parts: a block's each, or the wide rows' shares
+    const int64_t grid = grad_shape(rows, cols, 2, 16).grid;
+    int64_t parts = rows < kWideParts ? rows : kWideParts;
+    if (cols <= kNormCols && grid > parts) parts = grid;
+    return (size_t)parts * 2 * grad_stride(cols) * 4;
 }
 
-cudaError_t launch_norm(int dt, int param_dt, const NormArgs& a, cudaStream_t s) {
+cudaError_t launch_norm(int dt, const NormArgs& a, cudaStream_t s) {
     if (a.rows == 0 || a.cols == 0) return cudaSuccess;
-    if (dt == FSDP_F32) return param_dt == FSDP_F32 ? norm<float, float>(a, s) : norm<float, uint16_t>(a, s);
-    return param_dt == FSDP_F32 ? norm<uint16_t, float>(a, s) : norm<uint16_t, uint16_t>(a, s);
+    const cudaError_t e = dt == FSDP_F32 ? norm<float>(a, s) : norm<uint16_t>(a, s);
+    count_launch();
+    return e;
 }
 
-cudaError_t launch_norm_grad(int dt, int param_dt, int param_grad_dt, const NormGradArgs& a, cudaStream_t s) {
+cudaError_t launch_norm_grad(int dt, int param_grad_dt, const NormGradArgs& a, cudaStream_t s) {
     if (a.cols == 0) return cudaSuccess;
-    NormGradPlan p = {};
+    int parts = 0;
     if (a.rows > 0) {
-        p = grad_plan(a.rows, a.cols);
-        cudaError_t e;
-        if (dt == FSDP_F32)
-            e = param_dt == FSDP_F32 ? norm_grad_rows<float, float>(a, p, s) : norm_grad_rows<float, uint16_t>(a, p, s);
-        else
-            e = param_dt == FSDP_F32 ? norm_grad_rows<uint16_t, float>(a, p, s) : norm_grad_rows<uint16_t, uint16_t>(a, p, s);
+        const cudaError_t e = dt == FSDP_F32 ? norm_grad<float>(a, &parts, s) : norm_grad<uint16_t>(a, &parts, s);
         if (e != cudaSuccess) return e;
     }
     if (!a.grad_weight && !a.grad_bias) return cudaSuccess;
     const dim3 grid((unsigned)((a.cols + 31) / 32), 2);
-    if (param_grad_dt == FSDP_F32)
-        norm_join_kernel<float><<<grid, 256, 0, s>>>(a.work, p.stride, p.parts, a.cols, a.accumulate,
-                                                     static_cast<float*>(a.grad_weight), static_cast<float*>(a.grad_bias));
-    else
-        norm_join_kernel<uint16_t><<<grid, 256, 0, s>>>(a.work, p.stride, p.parts, a.cols, a.accumulate,
-                                                        static_cast<uint16_t*>(a.grad_weight), static_cast<uint16_t*>(a.grad_bias));
+    const float* work = a.work;
+    const int64_t stride = grad_stride(a.cols);
     count_launch();
-    return cudaGetLastError();
+    if (param_grad_dt == FSDP_F32)
+        return launch_next(norm_join_kernel<float>, grid, 32 * kJoinWarps, s, work, stride, parts, a.cols, a.accumulate,
+                           static_cast<float*>(a.grad_weight), static_cast<float*>(a.grad_bias));
+    return launch_next(norm_join_kernel<uint16_t>, grid, 32 * kJoinWarps, s, work, stride, parts, a.cols, a.accumulate,
+                       static_cast<uint16_t*>(a.grad_weight), static_cast<uint16_t*>(a.grad_bias));
 }
 
 }  // namespace fsdp

@@ -100,32 +100,178 @@ __device__ __forceinline__ void store_span(T* p, const Raw<T>& r, int n, int lan
         if (e >= first && e < last) store_elem(p + e, r, e);
 }
 
-// ------------------------------------------------------------- dropout mask
-
-// Philox4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel random numbers: as
-// easy as 1, 2, 3", 2011).
-__device__ __forceinline__ uint4 philox(uint4 c, uint32_t k0, uint32_t k1) {
-#pragma unroll
-    for (int i = 0; i < 10; ++i) {
-        const uint64_t a = (uint64_t)0xD2511F53u * c.x, b = (uint64_t)0xCD9E8D57u * c.z;
-        c = make_uint4((uint32_t)(b >> 32) ^ c.y ^ k0, (uint32_t)b, (uint32_t)(a >> 32) ^ c.w ^ k1, (uint32_t)a);
-        k0 += 0x9E3779B9u;
-        k1 += 0xBB67AE85u;
-    }
-    return c;
+// The granules of a warp's span, as load_granule and store_span do them, where
+// kAligned says that every row starts on the 16-byte grid and holds whole
+// granules (n is 8, or 0 past the row's end).
+template <bool kAligned, typename T>
+__device__ __forceinline__ void load_cols(Raw<T>& r, const T* row, int64_t c, int n) {
+    if constexpr (!kAligned)
+        load_granule(r, row, c, n);
+    else if (n)
+        load_aligned(r, row + c);
+}
+template <bool kAligned, typename T>
+__device__ __forceinline__ void store_cols(T* p, const Raw<T>& r, int n, int lane) {
+    if constexpr (!kAligned)
+        store_span(p, r, n, lane);
+    else if (n)
+        store_raw(p, r);
 }
 
-// Drops and scales the 8 columns 8 * block ... of a row. One generator block
-// serves them, 16 bits each: with 32 bits each, two blocks, the generator's
-// multiplications bound the kernel (1 GiB of bf16 on one GB300: 5004 GB/s
-// against 6563, and 6928 for the copy alone).
-__device__ __forceinline__ void drop(float (&x)[8], const Mask& m, int64_t row, uint32_t block) {
-    const uint4 r = philox(make_uint4(block, (uint32_t)row, (uint32_t)((uint64_t)row >> 32), m.draw), m.key0, m.key1);
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+// The 8 columns of a granule in binary32, as pairs: one instruction works on
+// two values, and these kernels are bound by instructions before memory.
+struct Cols {
+    float2 p[4];
+    __device__ __forceinline__ float get(int e) const { return e & 1 ? p[e >> 1].y : p[e >> 1].x; }
+    __device__ __forceinline__ void set(int e, float v) {
+        if (e & 1)
+            p[e >> 1].y = v;
+        else
+            p[e >> 1].x = v;
+    }
+};
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ Cols all(float v) { return {{both(v), both(v), both(v), both(v)}}; }
+__device__ __forceinline__ Cols operator+(const Cols& a, const Cols& b) {
+    Cols r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.p[i] = __fadd2_rn(a.p[i], b.p[i]);
+    return r;
+}
+__device__ __forceinline__ Cols operator*(const Cols& a, const Cols& b) {
+    Cols r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.p[i] = __fmul2_rn(a.p[i], b.p[i]);
+    return r;
+}
+__device__ __forceinline__ Cols fma(const Cols& a, const Cols& b, const Cols& c) {
+    Cols r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.p[i] = __ffma2_rn(a.p[i], b.p[i], c.p[i]);
+    return r;
+}
+// Sums over a granule, two columns at a time.
+__device__ __forceinline__ void sum_into(float2& s, const Cols& a) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s = __fadd2_rn(s, a.p[i]);
+}
+__device__ __forceinline__ void dot_into(float2& s, const Cols& a, const Cols& b) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s = __ffma2_rn(a.p[i], b.p[i], s);
+}
+
+__device__ __forceinline__ Cols widened(const Raw<uint16_t>& r) {
+    Cols x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        x.p[i] = make_float2(__uint_as_float(r.w[i] << 16), __uint_as_float(r.w[i] & 0xffff0000u));
+    return x;
+}
+__device__ __forceinline__ Cols widened(const Raw<float>& r) {
+    Cols x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x.p[i] = make_float2(__uint_as_float(r.w[2 * i]), __uint_as_float(r.w[2 * i + 1]));
+    return x;
+}
+// Rounded to a granule, NaN to some NaN: the data path's rule for a NaN's bits
+// takes eight comparisons a granule, and no sum here keeps them.
+__device__ __forceinline__ void round_to(const Cols& x, Raw<uint16_t>& r) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r.w[i]) : "f"(x.p[i].y), "f"(x.p[i].x));
+}
+__device__ __forceinline__ void round_to(const Cols& x, Raw<float>& r) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        x[2 * i] = (w[i] & 0xffffu) < m.limit ? x[2 * i] * m.scale : 0.0f;
-        x[2 * i + 1] = (w[i] >> 16) < m.limit ? x[2 * i + 1] * m.scale : 0.0f;
+        r.w[2 * i] = __float_as_uint(x.p[i].x);
+        r.w[2 * i + 1] = __float_as_uint(x.p[i].y);
+    }
+}
+// Columns past a row's end become 0.
+__device__ __forceinline__ void cut(Cols& x, int n) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (e >= n) x.set(e, 0.0f);
+}
+
+// -------------------------------------------------- rows on their way in
+
+// A warp's span of one row in shared memory, filled by asynchronous 16-byte
+// copies: the granules' blocks and, for a row off the 16-byte grid, one more.
+// The blocks are copied in the order of memory (a lane's own 32 bytes of fp32
+// would make every copy half a sector), so a warp meets between its copies'
+// arrival and its reads, and again before the next copies.
+template <bool kAligned, typename T>
+constexpr int kSlot = 32 * Raw<T>::kVec + (kAligned ? 0 : 1);
+
+__device__ __forceinline__ void async_copy(uint4* dst, uintptr_t src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+// Starts the copies of the 16-byte blocks that hold a row's columns c0 ...
+// c0 + 255; no block that lies wholly past the row's end is touched.
+template <bool kAligned, typename T>
+__device__ __forceinline__ void span_fetch(uint4* slot, const T* row, int c0, int cols, int lane) {
+    constexpr int kV = Raw<T>::kVec;
+    const uintptr_t from = reinterpret_cast<uintptr_t>(row + c0);
+    const int sh = kAligned ? 0 : (int)(from & 15u);
+    const int bytes = cols > c0 ? (cols - c0) * (int)sizeof(T) + sh : 0;
+#pragma unroll
+    for (int v = 0; v < kV + (kAligned ? 0 : 1); ++v) {
+        const int b = v * 32 + lane;
+        if ((v < kV || lane == 0) && b * 16 < bytes) async_copy(slot + b, from - sh + b * 16);
+    }
+}
+
+// The lane's granule of a span that has arrived; what it holds past the row's
+// end is not defined.
+template <bool kAligned, typename T>
+__device__ __forceinline__ void span_read(Raw<T>& r, const uint4* slot, const T* row, int c0, int lane) {
+    constexpr int kV = Raw<T>::kVec;
+    const unsigned sh = kAligned ? 0u : (unsigned)(reinterpret_cast<uintptr_t>(row + c0) & 15u);
+    uint4 b[kV + 1];
+#pragma unroll
+    for (int v = 0; v < kV; ++v) b[v] = slot[lane * kV + v];
+    if (kAligned || sh == 0) {
+#pragma unroll
+        for (int v = 0; v < kV; ++v) put(r.w + 4 * v, b[v]);
+        return;
+    }
+    b[kV] = slot[lane * kV + kV];
+#pragma unroll
+    for (int v = 0; v < kV; ++v) put(r.w + 4 * v, funnel(b[v], b[v + 1], sh));
+}
+
+// ------------------------------------------------------------- dropout mask
+
+// Adds to y the dropout of x, the 8 columns 8 * block ... of a row. The
+// generator is Philox4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel random
+// numbers: as easy as 1, 2, 3", 2011). One block of it serves 8 columns, 16
+// bits each: with 32 bits each, two blocks, its multiplications bound the
+// kernel (1 GiB of bf16 on one GB300: 5004 GB/s against 6563, and 6928 for the
+// copy alone).
+__device__ __forceinline__ void add_dropped(Cols& y, const Cols& x, const Mask& m, int64_t row, uint32_t block) {
+    uint32_t c0 = block, c1 = (uint32_t)row, c2 = (uint32_t)((uint64_t)row >> 32), c3 = m.draw;
+#pragma unroll
+    for (int i = 0; i < 10; ++i) {
+        const uint64_t a = (uint64_t)0xD2511F53u * c0, b = (uint64_t)0xCD9E8D57u * c2;
+        c0 = (uint32_t)(b >> 32) ^ c1 ^ m.key[2 * i];
+        c2 = (uint32_t)(a >> 32) ^ c3 ^ m.key[2 * i + 1];
+        c1 = (uint32_t)b;
+        c3 = (uint32_t)a;
+    }
+    const uint32_t w[4] = {c0, c1, c2, c3};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        // a word's lower bits do not decide on its upper half
+        if (w[i] << 16 < m.limit) y.p[i].x = __fmaf_rn(x.p[i].x, m.scale, y.p[i].x);
+        if (w[i] < m.limit) y.p[i].y = __fmaf_rn(x.p[i].y, m.scale, y.p[i].y);
     }
 }
 
@@ -137,10 +283,40 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
+// A row of a matrix whose row stride is below 2^32 bytes: one multiply-add.
+template <typename T>
+__device__ __forceinline__ T* row_at(void* data, uint32_t row, uint32_t stride_bytes) {
+    return reinterpret_cast<T*>(reinterpret_cast<uintptr_t>(data) + (uint64_t)row * stride_bytes);
+}
+
 // Columns of granule g of a row, 0 past its end.
-__device__ __forceinline__ int granule_cols(int64_t g, int64_t cols) {
-    const int64_t left = cols - g * kGran;
+template <typename I>
+__device__ __forceinline__ int granule_cols(I g, I cols) {
+    const I left = cols - g * kGran;
     return left >= kGran ? kGran : (left > 0 ? (int)left : 0);
+}
+
+// ----------------------------------------------------- launches in a chain
+
+// A kernel that follows another of the same call may be launched before that
+// one has ended (programmatic dependent launch), so that its start costs no
+// time of its own; it waits here before it touches what the other wrote.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the next kernel's blocks start as soon as all of this one's have.
+__device__ __forceinline__ void allow_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... A>
+cudaError_t launch_next(void (*kernel)(A...), dim3 grid, int block, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)block);
+    cfg.stream = s;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace

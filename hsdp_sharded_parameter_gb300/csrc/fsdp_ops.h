@@ -18,10 +18,19 @@ struct Mat {
     int64_t stride;
 };
 
-// The mask of a dropout. limit 65536: nothing is dropped.
+// Whether a matrix's rows all start on the 16-byte grid.
+inline bool on_grid(const Mat& m, int es) {
+    return reinterpret_cast<uintptr_t>(m.data) % 16 == 0 && m.stride * es % 16 == 0;
+}
+
+// The mask of a dropout: the generator's round keys (ten pairs, worked out
+// once on the host: as kernel arguments they are operands of the rounds'
+// instructions), and whether a 16-bit half is kept: half << 16 < limit.
 struct Mask {
-    uint32_t key0, key1, draw, limit;
-    float scale;  // 65536 / limit
+    uint32_t key[20];
+    uint32_t draw, limit;
+    int drops;    // 0: everything is kept as it is
+    float scale;  // of what is kept
 };
 
 struct EmbeddingArgs {
@@ -50,6 +59,7 @@ struct DropoutArgs {
 struct NormArgs {
     int64_t rows, cols;
     Mat x, res, hidden, out;  // res.data, hidden.data may be nullptr
+    int param_dt;
     const void *weight, *bias;
     float *mean, *rstd;
     float eps;
@@ -60,6 +70,7 @@ struct NormGradArgs {
     int64_t rows, cols;
     Mat grad, grad_hidden, hidden, grad_res, grad_x;
     const float *mean, *rstd;
+    int param_dt;
     const void* weight;
     void *grad_weight, *grad_bias;
     int accumulate;
@@ -77,7 +88,7 @@ size_t norm_grad_bytes(int64_t rows, int64_t cols);
 cudaError_t launch_embedding(int table_dt, int out_dt, const EmbeddingArgs& a, cudaStream_t s);
 cudaError_t launch_embedding_grad(int grad_dt, int table_dt, const EmbeddingGradArgs& a, cudaStream_t s);
 cudaError_t launch_dropout(int dt, const DropoutArgs& a, cudaStream_t s);
-cudaError_t launch_norm(int dt, int param_dt, const NormArgs& a, cudaStream_t s);
-cudaError_t launch_norm_grad(int dt, int param_dt, int param_grad_dt, const NormGradArgs& a, cudaStream_t s);
+cudaError_t launch_norm(int dt, const NormArgs& a, cudaStream_t s);
+cudaError_t launch_norm_grad(int dt, int param_grad_dt, const NormGradArgs& a, cudaStream_t s);
 
 }  // namespace fsdp

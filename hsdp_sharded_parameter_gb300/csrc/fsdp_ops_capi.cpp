@@ -78,11 +78,15 @@ int check_work(const char* what, const void* work, size_t have, size_t need) {
 int make_mask(const char* what, double p, uint64_t seed, uint32_t draw, int64_t cols, Mask& m) {
     if (!(p >= 0.0 && p <= 1.0)) return bad(what, "p is not in [0, 1]");
     if (cols > (int64_t)1 << 34) return bad(what, "too many columns");
-    m.key0 = (uint32_t)seed;
-    m.key1 = (uint32_t)(seed >> 32);
+    const int kept = (int)std::nearbyint((1.0 - p) * 65536.0);  // K of the header
+    for (uint32_t i = 0; i < 10; ++i) {
+        m.key[2 * i] = (uint32_t)seed + i * 0x9E3779B9u;
+        m.key[2 * i + 1] = (uint32_t)(seed >> 32) + i * 0xBB67AE85u;
+    }
     m.draw = draw;
-    m.limit = (uint32_t)std::nearbyint((1.0 - p) * 65536.0);
-    m.scale = m.limit ? (float)(65536.0 / m.limit) : 1.0f;
+    m.drops = kept < 65536;
+    m.limit = (uint32_t)kept << 16;
+    m.scale = kept ? (float)(65536.0 / kept) : 1.0f;
     return FSDP_OK;
 }
 
@@ -192,9 +196,9 @@ int fsdp_layer_norm(int64_t rows, int64_t cols, int dt, const void* x, int64_t x
     FSDP_TRY(check_float(what, "eps", eps));
     if (eps < 0) return bad(what, "eps is negative");
     NormArgs a = {rows, cols, mat(x, x_stride), mat(residual, residual_stride), mat(hidden, hidden_stride),
-                  mat(out, out_stride), weight, bias, mean, rstd, (float)eps, {}};
+                  mat(out, out_stride), param_dt, weight, bias, mean, rstd, (float)eps, {}};
     FSDP_TRY(make_mask(what, p, seed, draw, cols, a.mask));
-    return launched(launch_norm(dt, param_dt, a, stream), what);
+    return launched(launch_norm(dt, a, stream), what);
 }
 
 int fsdp_layer_norm_grad_workspace(int64_t rows, int64_t cols, size_t* bytes) {
@@ -236,9 +240,9 @@ int fsdp_layer_norm_grad(int64_t rows, int64_t cols, int dt, const void* grad_ou
     FSDP_TRY(check_work(what, workspace, workspace_bytes, norm_grad_bytes(rows, cols)));
     NormGradArgs a = {rows, cols, mat(grad_out, grad_out_stride), mat(grad_hidden, grad_hidden_stride),
                       mat(hidden, hidden_stride), mat(grad_residual, grad_residual_stride), mat(grad_x, grad_x_stride),
-                      mean, rstd, weight, grad_weight, grad_bias, accumulate ? 1 : 0, static_cast<float*>(workspace), {}};
+                      mean, rstd, param_dt, weight, grad_weight, grad_bias, accumulate ? 1 : 0, static_cast<float*>(workspace), {}};
     FSDP_TRY(make_mask(what, p, seed, draw, cols, a.mask));
-    return launched(launch_norm_grad(dt, param_dt, param_grad_dt, a, stream), what);
+    return launched(launch_norm_grad(dt, param_grad_dt, a, stream), what);
 }
 
 }  // extern "C"

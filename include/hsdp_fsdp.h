@@ -412,7 +412,8 @@ int fsdp_rs_ar_reduce_noalloc(fsdp_plan_t plan, int grad_dtype, const void* cons
  *
  * Numerics: everything between an operator's inputs and outputs is computed
  * and summed in binary32 and rounded once to the output's type. Sums are
- * taken in an order fixed by the sizes, so equal calls give equal bits. */
+ * taken in an order fixed by the sizes, so equal calls give equal bits. A
+ * result that is not a number is some NaN. */
 
 enum fsdp_index_type { FSDP_I32 = 0, FSDP_I64 = 1 };
 
