@@ -4,13 +4,14 @@
 // no row.
 //
 // Gradient: grad_table[v] = scale * sum of grad_out[t] over the tokens t of
-// row v. Three kernels:
-//   1. a stable radix sort of (row, token) by one cluster of blocks, while
-//      the other blocks write the zeros of the rows no token names;
-//   2. sums over chunks of sorted tokens: a warp adds up the gradients of a
-//      chunk for a span of 256 columns, writes the rows that lie inside the
-//      chunk and leaves the sums of rows that cross its ends;
-//   3. the rows that cross chunks: their partial sums added in order.
+// row v. Three kernels, each launched while the one before it runs:
+//   1. a stable radix sort of (row, token) by one cluster of blocks, which
+//      also marks the rows that a token names;
+//   2. sums: a warp adds up the gradients of a chunk of sorted tokens for a
+//      span of 256 columns, writes the rows that lie inside the chunk, leaves
+//      partial sums of those that cross its ends, and lists these;
+//   3. the partial sums of the listed rows, added in order, and beside them
+//      the zeros of the rows that are not marked.
 #include "fsdp_ops.cuh"
 
 namespace fsdp {
@@ -30,35 +31,58 @@ __device__ __forceinline__ int row_of(int64_t id, int64_t first, int64_t vocab) 
 
 // ------------------------------------------------------------------ forward
 
-template <typename S, typename D>
-__global__ void __launch_bounds__(32 * kEmbWarps) embedding_kernel(EmbeddingArgs a, int64_t spans, int64_t items) {
+// A warp takes up to kEmbSpans neighbouring spans of 256 columns of a token.
+constexpr int kEmbSpans = 4;
+
+template <typename S, typename D, bool kAligned>
+__global__ void __launch_bounds__(32 * kEmbWarps) embedding_kernel(EmbeddingArgs a, int64_t steps, int per, int64_t items) {
     const int lane = threadIdx.x & 31;
     for (int64_t it = warp_id(); it < items; it += warp_count()) {
-        const int64_t t = it / spans, g = (it - t * spans) * 32 + lane, c = g * kGran;
-        const int n = granule_cols(g, a.cols);
+        const int64_t t = it / steps, g0 = (it - t * steps) * (per * 32) + lane;
         const int64_t row = row_of(read_id(a.ids, a.wide_ids, t), a.first, a.vocab);
-        Raw<S> in;
-        Raw<D> out;
-        zero_raw(in);
-        if (row < a.vocab) load_granule(in, static_cast<const S*>(a.table.data) + row * a.table.stride, c, n);
-        round_to(row < a.vocab ? widened(in) * all(a.scale) : all(0.0f), out);
-        store_span(static_cast<D*>(a.out.data) + t * a.out.stride + c, out, n, lane);
+        const bool named = row < a.vocab;
+        const S* from = static_cast<const S*>(a.table.data) + row * a.table.stride;
+        D* to = static_cast<D*>(a.out.data) + t * a.out.stride;
+        Raw<S> in[kEmbSpans];
+#pragma unroll
+        for (int u = 0; u < kEmbSpans; ++u) {
+            const int64_t g = g0 + u * 32;
+            if (named && u < per) load_cols<kAligned>(in[u], from, g * kGran, granule_cols(g, a.cols));
+        }
+#pragma unroll
+        for (int u = 0; u < kEmbSpans; ++u) {
+            if (u >= per) break;
+            const int64_t g = g0 + u * 32;
+            Raw<D> r;
+            round_to(named ? widened(in[u]) * all(a.scale) : all(0.0f), r);
+            store_cols<kAligned>(to + g * kGran, r, granule_cols(g, a.cols), lane);
+        }
     }
 }
 
-// ------------------------------------------------- gradient: sort and zeros
+// ------------------------------------------------- gradient: the sort
 
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
-constexpr int kMaxBins = 256;
+constexpr int kMaxBits = 9;      // of a digit: the counts of 32 warps take half the shared memory
 constexpr int kSortCluster = 8;
+constexpr int kKeep = 8;         // tokens of a lane at a time
+constexpr int kTile = kSortThreads * kKeep;
+constexpr int kFewTokens = 512;  // ranked by comparisons
 
-// Workspace: the number of tokens that name a row, two buffers of sorted rows
-// and tokens, and the partial sums of rows that cross chunks ([chunk] for one
-// that began in an earlier chunk, [nchunks + chunk] for one that begins in
-// it), stride columns each.
+// A row whose tokens lie in chunks first, first + 1, ..., first + more.
+struct Crossing {
+    int row, first, more, unused;
+};
+
+// Workspace: how many tokens name a row and how many rows cross chunks, two
+// buffers of sorted tokens, the marked rows, the rows that cross, and their partial
+// sums ([chunk] for a row that began in an earlier chunk, [nchunks + chunk]
+// for one that begins in it), stride columns each.
 struct GradWork {
-    int* count;
-    int *rows[2], *toks[2];
+    int *count, *crossings;
+    int2* sorted[2];  // (row, token)
+    uint32_t* marks;  // a bit for each row
+    Crossing* cross;
     float* part;
     int64_t stride;
     int chunk, nchunks;
@@ -66,22 +90,29 @@ struct GradWork {
 
 int64_t up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
 
-// Tokens of a chunk.
-int chunk_tokens(int64_t) { return 32; }
+// Tokens of a chunk: few while that gives no more warps than the GPU holds at
+// once (the fewer, the sooner the longest is done), else 32.
+int chunk_tokens(int64_t n, int64_t cols) {
+    const int64_t spans = (cols + kSpan - 1) / kSpan, warps = 64 * (int64_t)sm_count();
+    return n * spans <= 8 * warps ? 8 : (n * spans <= 16 * warps ? 16 : 32);
+}
 
-GradWork grad_work(void* work, int64_t n, int64_t cols, size_t* bytes) {
+GradWork grad_work(void* work, int64_t n, int64_t vocab, int64_t cols, size_t* bytes) {
     GradWork w;
     char* p = static_cast<char*>(work);
     size_t at = 256;
     w.count = reinterpret_cast<int*>(p);
+    w.crossings = w.count + 1;
     for (int i = 0; i < 2; ++i) {
-        w.rows[i] = reinterpret_cast<int*>(p + at);
-        at += up(n * 4, 256);
-        w.toks[i] = reinterpret_cast<int*>(p + at);
-        at += up(n * 4, 256);
+        w.sorted[i] = reinterpret_cast<int2*>(p + at);
+        at += up(n * 8, 256);
     }
-    w.chunk = chunk_tokens(n);
+    w.marks = reinterpret_cast<uint32_t*>(p + at);
+    at += up((vocab + 31) / 32 * 4, 256);
+    w.chunk = chunk_tokens(n, cols);
     w.nchunks = (int)((n + w.chunk - 1) / w.chunk);
+    w.cross = reinterpret_cast<Crossing*>(p + at);
+    at += up((int64_t)w.nchunks * sizeof(Crossing), 256);
     w.stride = up(cols, kGran);
     w.part = reinterpret_cast<float*>(p + at);
     at += (size_t)2 * w.nchunks * w.stride * 4;
@@ -101,171 +132,270 @@ __device__ __forceinline__ uint32_t cluster_read(const uint32_t* p, int rank) {
     return v;
 }
 
+// Shared memory of the sort: a tile of tokens in their new order, each warp's
+// count of each digit and the lanes that hold it (rows of an odd length, so
+// that warps and digits spread over the banks), the block's counts, where each
+// digit's tokens of this block go, and where they begin in the tile.
 struct SortSmem {
-    uint32_t hist[kSortWarps][kMaxBins];
-    uint32_t total[kMaxBins + 1];  // of this block; [kMaxBins]: tokens that name a row
-    uint32_t base[kMaxBins];
-    uint32_t scan[kMaxBins / 32];
+    int2* tile;
+    uint32_t *hist, *lanes, *total, *base, *start, *scan;
+    int pitch;
+    __device__ SortSmem(void* p, int bins) : pitch(bins | 1) {
+        tile = static_cast<int2*>(p);
+        hist = reinterpret_cast<uint32_t*>(tile + kTile);
+        lanes = hist + kSortWarps * pitch;
+        total = lanes + kSortWarps * pitch;
+        base = total + bins + 1;  // total[bins]: the block's tokens that name a row
+        start = base + bins;
+        scan = start + bins;
+    }
+    static size_t bytes(int bins) {
+        return 8 * kTile + 4 * (size_t)(2 * kSortWarps * (bins | 1) + 3 * bins + 1 + 2 * kSortWarps);
+    }
 };
 
-// One pass over this block's part of the tokens: their digit's counts, the
-// places the counts of all blocks give them, and the move. Tokens keep their
-// order within a digit: a warp's tokens are consecutive and it ranks 32 of
-// them at a time by the lanes that hold the same digit.
-template <typename Read>
-__device__ void sort_pass(SortSmem& sm, int64_t n, int blocks, int rank, int shift, int bits, bool first,
-                          int64_t vocab, Read read, int* rows_out, int* toks_out) {
+// The sums of the block's threads' two values before this one.
+__device__ __forceinline__ uint2 block_scan(const SortSmem& sm, uint2 v, int lane, int warp) {
+    uint2 incl = v;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+        const uint32_t x = __shfl_up_sync(kFull, incl.x, s), y = __shfl_up_sync(kFull, incl.y, s);
+        if (lane >= s) {
+            incl.x += x;
+            incl.y += y;
+        }
+    }
+    if (lane == 31) {
+        sm.scan[2 * warp] = incl.x;
+        sm.scan[2 * warp + 1] = incl.y;
+    }
+    __syncthreads();
+    const uint32_t x = __reduce_add_sync(kFull, lane < warp ? sm.scan[2 * lane] : 0);
+    const uint32_t y = __reduce_add_sync(kFull, lane < warp ? sm.scan[2 * lane + 1] : 0);
+    return make_uint2(x + incl.x - v.x, y + incl.y - v.y);
+}
+
+// A digit's counts before each warp, and their total: a thread adds down a
+// column.
+__device__ __forceinline__ uint32_t column_sums(const SortSmem& sm, int d) {
+    uint32_t sum = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) {
+        const uint32_t c = sm.hist[w * sm.pitch + d];
+        sm.hist[w * sm.pitch + d] = sum;
+        sum += c;
+    }
+    return sum;
+}
+
+// One pass over this block's part of the tokens: its digits' counts, the
+// places that the counts of all blocks give them, and the move. Tokens keep
+// their order within a digit: a warp's tokens of a tile are consecutive, and
+// it ranks 32 of them at a time by the lanes that hold the same digit, which
+// meet in a word of shared memory (a vote for each bit, or a match over the
+// warp, is 1400 cycles and more for a step of 32 warps). A tile is put in order in shared
+// memory and written from there, neighbours to neighbouring places.
+__device__ __forceinline__ void sort_pass(const EmbeddingGradArgs& a, const SortSmem& sm, int blocks, int rank, int shift,
+                                          int bits, const int2* in, int2* out) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int bins = 1 << bits;
-    const int64_t per = ((n + blocks - 1) / blocks + kSortWarps * 32 - 1) / (kSortWarps * 32) * 32;  // of a warp
-    const int64_t lo = (rank * (int64_t)kSortWarps + warp) * per;
-    const int64_t hi = lo + per < n ? lo + per : n;
-    for (int i = lane; i < bins; i += 32) sm.hist[warp][i] = 0;
-    if (first && tid == 0) sm.total[kMaxBins] = 0;
-    __syncthreads();
-    int named = 0;
-    for (int64_t i = lo; i < hi; i += 32) {
-        int row = 0, tok;
-        const bool on = i + lane < hi;
-        if (on) read(i + lane, row, tok);
-        const int d = on ? (row >> shift) & (bins - 1) : bins;
-        const unsigned peers = __match_any_sync(kFull, d);
-        if (on && lane == __ffs(peers) - 1) sm.hist[warp][d] += __popc(peers);
-        if (first) named += __popc(__ballot_sync(kFull, on && row < vocab));
-        __syncwarp();
-    }
-    if (first && lane == 0 && named) atomicAdd(&sm.total[kMaxBins], (uint32_t)named);
-    __syncthreads();
-    if (tid < bins) {
-        uint32_t s = 0;
-        for (int w = 0; w < kSortWarps; ++w) {
-            const uint32_t t = sm.hist[w][tid];
-            sm.hist[w][tid] = s;
-            s += t;
-        }
-        sm.total[tid] = s;
-    }
-    cluster_sync();
-    uint32_t before = 0, all = 0, incl = 0;
-    if (tid < kMaxBins) {
-        if (tid < bins)
-            for (int r = 0; r < blocks; ++r) {
-                const uint32_t t = cluster_read(&sm.total[tid], r);
-                if (r < rank) before += t;
-                all += t;
+    const int bins = 1 << bits, n = (int)a.n, per = (n + blocks - 1) / blocks;
+    const int64_t from = (int64_t)rank * per;
+    const int lo = (int)(from < n ? from : n), hi = from + per < n ? (int)(from + per) : n;
+    const bool one = hi - lo <= kTile;
+    uint32_t* const hist = sm.hist + warp * sm.pitch;
+    uint32_t* const lanes = sm.lanes + warp * sm.pitch;
+    int2 tok[kKeep];
+    uint32_t before[kKeep];  // the warp's tokens of the same digit before this one
+    int steps = 0;           // of 32 tokens, for each warp
+    // a lane's tokens of the tile at b, -1 where there is none
+    auto load = [&](int b) {
+        steps = hi - b < kTile ? (hi - b + kSortThreads - 1) / kSortThreads : kKeep;
+#pragma unroll
+        for (int k = 0; k < kKeep; ++k) {
+            const int i = b + (warp * steps + k) * 32 + lane;
+            tok[k] = make_int2(-1, i);
+            if (k < steps && i < hi) {
+                if (in)
+                    tok[k] = __ldcg(in + i);
+                else
+                    tok[k].x = row_of(read_id(a.ids, a.wide_ids, i), a.first, a.vocab);
             }
-        incl = all;
-        for (int d = 1; d < 32; d <<= 1) {
-            const uint32_t t = __shfl_up_sync(kFull, incl, d);
-            if (lane >= d) incl += t;
         }
-        if (lane == 31) sm.scan[warp] = incl;
+    };
+    auto clear = [&] {
+        for (int i = tid; i < kSortWarps * sm.pitch; i += kSortThreads) sm.hist[i] = sm.lanes[i] = 0;
+        __syncthreads();
+    };
+    auto count = [&] {
+        int named = 0;
+#pragma unroll
+        for (int k = 0; k < kKeep; ++k)
+            if (k < steps) {
+                const bool on = tok[k].x >= 0;
+                const int d = (tok[k].x >> shift) & (bins - 1);
+                if (on) atomicOr(lanes + d, 1u << lane);
+                __syncwarp();
+                const uint32_t peers = on ? lanes[d] : 0, seen = on ? hist[d] : 0;
+                __syncwarp();
+                if (on && lane == __ffs(peers) - 1) {
+                    hist[d] = seen + __popc(peers);
+                    lanes[d] = 0;
+                }
+                __syncwarp();
+                before[k] = seen + __popc(peers & ((1u << lane) - 1));
+                named += on && tok[k].x < a.vocab;
+            }
+        return named;
+    };
+
+    if (one) load(lo);
+    if (tid == 0) sm.total[bins] = 0;
+    clear();
+    int named = 0;
+#pragma unroll 1
+    for (int b = lo; b < hi; b += kTile) {
+        if (!one) load(b);
+        named += count();
+    }
+    named = __reduce_add_sync(kFull, named);
+    if (lane == 0 && named) atomicAdd(&sm.total[bins], (uint32_t)named);
+    __syncthreads();
+    uint32_t mine = 0;  // the digit's tokens in the tile at hand
+    if (tid < bins) sm.total[tid] = mine = column_sums(sm, tid);
+    cluster_sync();
+    // the digit's tokens in all blocks and in those before this one, and the scan over digits
+    uint32_t below = 0, sum = 0;
+    if (tid < bins)
+#pragma unroll
+        for (int r = 0; r < kSortCluster; ++r) {
+            const uint32_t t = r < blocks ? cluster_read(&sm.total[tid], r) : 0;
+            if (r < rank) below += t;
+            sum += t;
+        }
+    const uint2 at = block_scan(sm, make_uint2(sum, mine), lane, warp);
+    if (tid < bins) {
+        sm.base[tid] = at.x + below;
+        sm.start[tid] = at.y;
     }
     __syncthreads();
-    if (tid < kMaxBins) {
-        for (int w = 0; w < warp; ++w) incl += sm.scan[w];
-        sm.base[tid] = incl - all + before;
-    }
-    __syncthreads();
-    for (int64_t i = lo; i < hi; i += 32) {
-        int row = 0, tok = 0;
-        const bool on = i + lane < hi;
-        if (on) read(i + lane, row, tok);
-        const int d = on ? (row >> shift) & (bins - 1) : bins;
-        const unsigned peers = __match_any_sync(kFull, d);
-        if (on) {
-            const uint32_t at = sm.base[d] + sm.hist[warp][d] + __popc(peers & ((1u << lane) - 1));
-            rows_out[at] = row;
-            toks_out[at] = tok;
+#pragma unroll 1
+    for (int b = lo; b < hi; b += kTile) {
+        if (!one) {
+            load(b);
+            clear();
+            count();
+            __syncthreads();
+            if (tid < bins) mine = column_sums(sm, tid);
+            const uint32_t begin = block_scan(sm, make_uint2(0, mine), lane, warp).y;
+            if (tid < bins) sm.start[tid] = begin;
+            __syncthreads();
         }
-        __syncwarp();
-        if (on && lane == __ffs(peers) - 1) sm.hist[warp][d] += __popc(peers);
-        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < kKeep; ++k)
+            if (k < steps && tok[k].x >= 0) {
+                const int d = (tok[k].x >> shift) & (bins - 1);
+                sm.tile[sm.start[d] + hist[d] + before[k]] = tok[k];
+            }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kKeep; ++k) {
+            const int i = k * kSortThreads + tid;
+            if (i < hi - b) {
+                const int2 x = sm.tile[i];
+                const int d = (x.x >> shift) & (bins - 1);
+                out[sm.base[d] + i - sm.start[d]] = x;
+            }
+        }
+        if (one) break;
+        __syncthreads();
+        if (tid < bins) sm.base[tid] += mine;
     }
     // the moved tokens reach the cluster's other blocks, and the totals may go
     cluster_sync();
 }
 
-// Blocks 0 .. blocks-1, one cluster, sort; the others write the zeros of the
-// rows that no token names, each for a range of rows whose tokens it looks
-// for among all ids.
-template <typename D>
+// The blocks, one cluster, sort the tokens by row.
 __global__ void __launch_bounds__(kSortThreads)
-    embedding_sort_kernel(EmbeddingGradArgs a, GradWork w, int blocks, int passes, int bits) {
-    extern __shared__ uint32_t raw_smem[];
-    if ((int)blockIdx.x < blocks) {
-        SortSmem& sm = *reinterpret_cast<SortSmem*>(raw_smem);
-        const int rank = blockIdx.x;
-        for (int p = 0; p < passes; ++p) {
-            int *ro = w.rows[p & 1], *to = w.toks[p & 1];
-            if (p == 0) {
-                sort_pass(sm, a.n, blocks, rank, 0, bits, true, a.vocab,
-                          [&](int64_t i, int& row, int& tok) {
-                              row = row_of(read_id(a.ids, a.wide_ids, i), a.first, a.vocab);
-                              tok = (int)i;
-                          },
-                          ro, to);
-                if (rank == 0 && threadIdx.x == 0) {
-                    uint32_t c = 0;
-                    for (int r = 0; r < blocks; ++r) c += cluster_read(&sm.total[kMaxBins], r);
-                    *w.count = (int)c;
-                }
-            } else {
-                const int *ri = w.rows[(p & 1) ^ 1], *ti = w.toks[(p & 1) ^ 1];
-                sort_pass(sm, a.n, blocks, rank, p * bits, bits, false, a.vocab,
-                          [&](int64_t i, int& row, int& tok) {
-                              row = __ldcg(ri + i);
-                              tok = __ldcg(ti + i);
-                          },
-                          ro, to);
-            }
-        }
-        cluster_sync();  // no block leaves while another reads its counts
-        return;
+    embedding_sort_kernel(EmbeddingGradArgs a, GradWork w, int passes, int bits) {
+    extern __shared__ uint4 raw_smem[];
+    allow_next();
+    const int blocks = gridDim.x, rank = blockIdx.x, tid = threadIdx.x;
+    const SortSmem sm(raw_smem, 1 << bits);
+    if (rank == 0 && tid == 0) *w.crossings = 0;
+    if (!a.accumulate)
+        for (int64_t i = rank * kSortThreads + tid; i < (a.vocab + 31) / 32; i += blocks * kSortThreads) w.marks[i] = 0;
+#pragma unroll 1
+    for (int p = 0; p < passes; ++p)
+        sort_pass(a, sm, blocks, rank, p * bits, bits, p ? w.sorted[(p & 1) ^ 1] : nullptr, w.sorted[p & 1]);
+    if (rank == 0 && tid == 0) {
+        int count = 0;
+#pragma unroll
+        for (int r = 0; r < kSortCluster; ++r)
+            if (r < blocks) count += (int)cluster_read(&sm.total[1 << bits], r);
+        *w.count = count;
     }
-    // zeros
-    const int64_t nz = gridDim.x - blocks, z = blockIdx.x - blocks;
-    const int64_t r0 = a.vocab * z / nz, r1 = a.vocab * (z + 1) / nz;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    constexpr int64_t kRows = 32 * 4096;  // rows whose bits fit the block's shared memory
-    for (int64_t b = r0; b < r1; b += kRows) {
-        const int64_t e = b + kRows < r1 ? b + kRows : r1;
-        for (int i = tid; i < (e - b + 31) / 32; i += kSortThreads) raw_smem[i] = 0;
-        __syncthreads();
-        for (int64_t i = tid; i < a.n; i += kSortThreads) {
-            const int64_t v = row_of(read_id(a.ids, a.wide_ids, i), a.first, a.vocab);
-            if (v >= b && v < e) atomicOr(&raw_smem[(v - b) >> 5], 1u << ((v - b) & 31));
+    if (!a.accumulate) {
+        // a row's first token marks it
+        const int2* sorted = w.sorted[(passes - 1) & 1];
+#pragma unroll 4
+        for (int64_t i = rank * kSortThreads + tid; i < a.n; i += blocks * kSortThreads) {
+            const int row = __ldcg(&sorted[i].x), prev = i > 0 ? __ldcg(&sorted[i - 1].x) : -1;
+            if (row != prev && row < a.vocab) atomicOr(w.marks + (row >> 5), 1u << (row & 31));
         }
-        __syncthreads();
-        const Raw<D> none = {};
-        const int64_t spans = (a.cols + kSpan - 1) / kSpan;
-        for (int64_t it = warp; it < (e - b) * spans; it += kSortWarps) {
-            const int64_t r = it / spans, g = (it - r * spans) * 32 + lane;
-            if (raw_smem[r >> 5] >> (r & 31) & 1) continue;
-            store_span(static_cast<D*>(a.table.data) + (b + r) * a.table.stride + g * kGran, none,
-                       granule_cols(g, a.cols), lane);
-        }
-        __syncthreads();
     }
+    cluster_sync();  // no block leaves while another reads its counts
 }
 
-// ------------------------------------------------------------ gradient: sums
+// The same for up to kFewTokens tokens, one block: a token's place is the
+// number of tokens that come before it.
+__global__ void __launch_bounds__(kFewTokens) embedding_few_kernel(EmbeddingGradArgs a, GradWork w) {
+    __shared__ int4 keys[kFewTokens / 4];
+    __shared__ int named;
+    allow_next();
+    const int tid = threadIdx.x, n = (int)a.n;
+    const int row = tid < n ? row_of(read_id(a.ids, a.wide_ids, tid), a.first, a.vocab) : 0x7fffffff;
+    reinterpret_cast<int*>(keys)[tid] = row;
+    if (tid == 0) {
+        named = 0;
+        *w.crossings = 0;
+    }
+    if (!a.accumulate)
+        for (int64_t i = tid; i < (a.vocab + 31) / 32; i += kFewTokens) w.marks[i] = 0;
+    __syncthreads();
+    int at = 0;
+    if (tid < n) {
+        for (int j = 0; j < (n + 3) / 4; ++j) {
+            const int4 k = keys[j];
+            at += (k.x < row || (k.x == row && 4 * j < tid)) + (k.y < row || (k.y == row && 4 * j + 1 < tid)) +
+                  (k.z < row || (k.z == row && 4 * j + 2 < tid)) + (k.w < row || (k.w == row && 4 * j + 3 < tid));
+        }
+        w.sorted[0][at] = make_int2(row, tid);
+        if (row < a.vocab) {
+            atomicAdd(&named, 1);
+            if (!a.accumulate) atomicOr(w.marks + (row >> 5), 1u << (row & 31));
+        }
+    }
+    __syncthreads();
+    if (tid == 0) *w.count = named;
+}
+
+// ------------------------------------------------------------ gradient: zeros and sums
 
 // Scales a row's sums, adds what the table holds where the caller wants it,
 // rounds and stores them.
-template <typename D>
+template <typename D, bool kAligned>
 __device__ __forceinline__ void store_row(const EmbeddingGradArgs& a, int row, int64_t g, Cols x, int lane) {
     const int n = granule_cols(g, a.cols);
     D* p = static_cast<D*>(a.table.data) + row * a.table.stride + g * kGran;
     Raw<D> r;
     x = x * all(a.scale);
     if (a.accumulate) {
-        load_granule(r, p - g * kGran, g * kGran, n);
+        load_cols<kAligned>(r, p - g * kGran, g * kGran, n);
         x = x + widened(r);
         __syncwarp();  // a shifted load reads its neighbours' blocks
     }
     round_to(x, r);
-    store_span(p, r, n, lane);
+    store_cols<kAligned>(p, r, n, lane);
 }
 
 __device__ __forceinline__ void store_part(float* p, const Cols& x) {
@@ -278,52 +408,95 @@ __device__ __forceinline__ Cols load_part(const float* p) {
     return {{make_float2(u.x, u.y), make_float2(u.z, u.w), make_float2(v.x, v.y), make_float2(v.z, v.w)}};
 }
 
-template <typename S, typename D>
-__global__ void __launch_bounds__(32 * kEmbWarps)
-    embedding_sum_kernel(EmbeddingGradArgs a, GradWork w, const int* rows, const int* toks, int64_t spans) {
-    constexpr int kU = 4;
+// Lists a row that begins in a chunk and reaches further ones: the last is
+// found among the chunks' first tokens, 32 probes at a time.
+__device__ __forceinline__ void list_crossing(const GradWork& w, const int2* sorted, int count, int row, int chunk, int lane) {
+    int lo = chunk + 1, hi = (count + w.chunk - 1) / w.chunk;  // chunk lo begins with the row, chunk hi does not
+    while (hi - lo > 1) {
+        const int gap = (hi - lo + 32) / 33, at = lo + (lane + 1) * gap;
+        const unsigned more = __popc(__ballot_sync(kFull, at < hi && __ldcg(&sorted[at * w.chunk].x) == row));
+        hi = lo + (int)(more + 1) * gap < hi ? lo + (int)(more + 1) * gap : hi;
+        lo += (int)more * gap;
+    }
+    if (lane == 0) w.cross[atomicAdd(w.crossings, 1)] = Crossing{row, chunk, lo - chunk, 0};
+}
+
+// Zeros for a row of n elements, by one warp.
+template <typename D>
+__device__ __forceinline__ void zero_row(D* row, int64_t n, int lane) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(row), end = reinterpret_cast<uintptr_t>(row + n);
+    const uintptr_t body = (p + 15) & ~(uintptr_t)15, tail = end & ~(uintptr_t)15;
+    if (body >= tail) {
+        for (int64_t i = lane; i < n; i += 32) row[i] = D(0);
+        return;
+    }
+    if (p + lane * sizeof(D) < body) row[lane] = D(0);
+    if (tail + lane * sizeof(D) < end) reinterpret_cast<D*>(tail)[lane] = D(0);
+#pragma unroll 4
+    for (uintptr_t q = body + lane * 16; q < tail; q += 512) st_stream(reinterpret_cast<uint4*>(q), make_uint4(0, 0, 0, 0));
+}
+
+// Block z writes the zeros of its rows, per for each warp (a power of two up to
+// 32, so that their marks lie in one word), that are not marked; marks NULL:
+// none is. Many short blocks: 131072 rows of 32 KB take 575 us in blocks of 8
+// rows and 656 in two blocks an SM that each take a long range.
+template <typename D>
+__device__ __forceinline__ void write_zeros(const EmbeddingGradArgs& a, const uint32_t* marks, int64_t z, int per) {
+    const int lane = threadIdx.x & 31;
+    const int64_t r0 = (z * kEmbWarps + (threadIdx.x >> 5)) * per;
+    if (r0 >= a.vocab) return;
+    const uint32_t named = marks ? __ldcg(marks + (r0 >> 5)) >> (r0 & 31) : 0u;
+    for (int i = 0; i < per && r0 + i < a.vocab; ++i)
+        if (!(named >> i & 1)) zero_row(static_cast<D*>(a.table.data) + (r0 + i) * a.table.stride, a.cols, lane);
+}
+
+// Tokens whose gradients a lane has in flight.
+template <typename S>
+constexpr int kFlight = sizeof(S) == 4 ? 4 : 8;
+
+template <typename S, typename D, bool kAligned>
+__global__ void __launch_bounds__(32 * kEmbWarps, 3)
+    embedding_sum_kernel(EmbeddingGradArgs a, GradWork w, const int2* sorted, int spans) {
+    constexpr int kU = kFlight<S>;
     const int lane = threadIdx.x & 31;
     const int64_t it = warp_id();
-    const int64_t chunk = it / spans, span = it - chunk * spans;
-    const int count = __ldg(w.count);
-    const int64_t lo = chunk * w.chunk;
-    if (lo >= count) return;
-    const int hi = (int)(lo + w.chunk < count ? lo + w.chunk : count);
-    const int64_t g = span * 32 + lane, c = g * kGran;
-    const int n = granule_cols(g, a.cols);
-    const int prev = lo > 0 ? __ldg(rows + lo - 1) : -1;
-    const int next = hi < count ? __ldg(rows + hi) : -1;
+    const int64_t chunk = it / spans;
+    const int g = (int)(it - chunk * spans) * 32 + lane, n = granule_cols((int64_t)g, a.cols);
+    const int64_t c = (int64_t)g * kGran;
+    wait_for_previous();
+    allow_next();  // not before: the next kernel's zeros need the sort's marks
+    const int count = __ldcg(w.count);
+    if (chunk * w.chunk >= count) return;
+    const int lo = (int)chunk * w.chunk, m = count - lo < w.chunk ? count - lo : w.chunk;
+    const int2 mine = lane < m ? __ldcg(sorted + lo + lane) : make_int2(-1, 0);
+    const int prev = lo > 0 ? __ldcg(&sorted[lo - 1].x) : -1;
+    const int next = lo + m < count ? __ldcg(&sorted[lo + m].x) : -1;
     Cols acc = all(0.0f);
     int cur = -1;
     bool open = false;  // cur began in an earlier chunk
-    for (int b = (int)lo; b < hi; b += 32) {
-        const int m = hi - b < 32 ? hi - b : 32;
-        const int my_row = lane < m ? __ldg(rows + b + lane) : -1, my_tok = lane < m ? __ldg(toks + b + lane) : 0;
-        for (int j = 0; j < m; j += kU) {
-            Raw<S> in[kU];
+    for (int j = 0; j < m; j += kU) {
+        Raw<S> in[kU];
 #pragma unroll
-            for (int u = 0; u < kU; ++u) {
-                const int64_t t = __shfl_sync(kFull, my_tok, (j + u) & 31);
-                if (j + u < m) load_granule(in[u], static_cast<const S*>(a.grad.data) + t * a.grad.stride, c, n);
-            }
+        for (int u = 0; u < kU; ++u) {
+            const int64_t t = __shfl_sync(kFull, mine.y, (j + u) & 31);
+            if (j + u < m) load_cols<kAligned>(in[u], static_cast<const S*>(a.grad.data) + t * a.grad.stride, c, n);
+        }
 #pragma unroll
-            for (int u = 0; u < kU; ++u) {
-                if (j + u >= m) break;
-                const int row = __shfl_sync(kFull, my_row, (j + u) & 31);
-                const Cols x = widened(in[u]);
-                if (row != cur) {
-                    if (cur >= 0) {
-                        if (!open)
-                            store_row<D>(a, cur, g, acc, lane);
-                        else if (n)
-                            store_part(w.part + chunk * w.stride + c, acc);
-                    }
-                    open = cur < 0 && row == prev;
-                    cur = row;
-                    acc = x;
-                } else {
-                    acc = acc + x;
+        for (int u = 0; u < kU; ++u) {
+            const int row = __shfl_sync(kFull, mine.x, (j + u) & 31);
+            if (j + u >= m) break;
+            if (row != cur) {
+                if (cur >= 0) {
+                    if (!open)
+                        store_row<D, kAligned>(a, cur, g, acc, lane);
+                    else if (n)
+                        store_part(w.part + chunk * w.stride + c, acc);
                 }
+                open = cur < 0 && row == prev;
+                cur = row;
+                acc = widened(in[u]);
+            } else {
+                acc = acc + widened(in[u]);
             }
         }
     }
@@ -331,115 +504,153 @@ __global__ void __launch_bounds__(32 * kEmbWarps)
         if (n) store_part(w.part + chunk * w.stride + c, acc);
     } else if (cur == next) {
         if (n) store_part(w.part + (w.nchunks + chunk) * w.stride + c, acc);
+        if (g < 32) list_crossing(w, sorted, count, cur, (int)chunk, lane);  // once, with the first span
     } else {
-        store_row<D>(a, cur, g, acc, lane);
+        store_row<D, kAligned>(a, cur, g, acc, lane);
     }
 }
 
-// Block (span, y): the rows that cross chunk ends y + 1, y + 1 + gridDim.y,
-// ... and began in the chunk before that end.
-template <typename D>
-__global__ void __launch_bounds__(32 * kEmbWarps)
-    embedding_join_kernel(EmbeddingGradArgs a, GradWork w, const int* rows) {
-    __shared__ float part[kEmbWarps][kSpan];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t g = (int64_t)blockIdx.x * 32 + lane, c = g * kGran;
+// The sum of a crossing row's parts p0 ... p1 - 1: the first chunk's tail, then
+// what the others leave at their heads.
+__device__ __forceinline__ Cols sum_parts(const GradWork& w, const int4& x, int p0, int p1, int64_t c) {
+    Cols acc = all(0.0f);
+#pragma unroll 4
+    for (int p = p0; p < p1; ++p) acc = acc + load_part(w.part + (x.y + p + (p == 0 ? w.nchunks : 0)) * w.stride + c);
+    return acc;
+}
+
+// The first spans * y blocks, block (span, y): the rows that cross chunks, for
+// a span of columns. Its warps take the listed rows of up to kShort parts in
+// turn, one each, and then the others together, a share of the parts each. The
+// other blocks write zeros and need not wait for the sums (no block of which
+// allowed this kernel before the sort, whose marks they read, had ended); the
+// last one does so in the end, that this kernel may not end before the sums.
+constexpr int kShort = 8;
+template <typename D, bool kAligned>
+__global__ void __launch_bounds__(32 * kEmbWarps) embedding_join_kernel(EmbeddingGradArgs a, GradWork w, int spans, int ys, int per) {
+    __shared__ float4 sums[kEmbWarps][2][32];
+    if ((int)blockIdx.x >= spans * ys) {
+        write_zeros<D>(a, w.nchunks ? w.marks : nullptr, blockIdx.x - spans * ys, per);
+        if (blockIdx.x + 1 == gridDim.x) wait_for_previous();
+        return;
+    }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, y = blockIdx.x / spans;
+    const int64_t g = (int64_t)(blockIdx.x - y * spans) * 32 + lane, c = g * kGran;
     const int n = granule_cols(g, a.cols);
-    const int count = __ldg(w.count);
-    for (int64_t b = blockIdx.y + 1; b * w.chunk < count; b += gridDim.y) {
-        const int row = __ldg(rows + b * w.chunk);
-        if (__ldg(rows + b * w.chunk - 1) != row) continue;
-        if (b > 1 && __ldg(rows + (b - 1) * w.chunk - 1) == row) continue;
-        int lo = (int)(b * w.chunk), hi = count;  // the row's last token: rows[lo] == row, rows[hi] > row
-        while (hi - lo > 1) {
-            const int mid = lo + (hi - lo) / 2;
-            if (__ldg(rows + mid) == row)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        // partial sums b - 1 (its tail), b, ..., last, a share for each warp
-        const int64_t last = lo / w.chunk, parts = last - b + 2;
-        const int64_t p0 = parts * warp / kEmbWarps, p1 = parts * (warp + 1) / kEmbWarps;
-        Cols acc = all(0.0f);
-        if (n)
-            for (int64_t p = p0; p < p1; ++p)
-                acc = acc + load_part(w.part + (p == 0 ? w.nchunks + b - 1 : b - 1 + p) * w.stride + c);
-        store_part(&part[warp][lane * kGran], acc);
+    wait_for_previous();
+    const int crossings = __ldcg(w.crossings);
+    for (int i = y * kEmbWarps + warp; i < crossings; i += ys * kEmbWarps) {
+        const int4 x = __ldcg(reinterpret_cast<const int4*>(w.cross + i));
+        if (x.z >= kShort) continue;
+        store_row<D, kAligned>(a, x.x, g, n ? sum_parts(w, x, 0, x.z + 1, c) : all(0.0f), lane);
+    }
+    for (int i = y; i < crossings; i += ys) {
+        const int4 x = __ldcg(reinterpret_cast<const int4*>(w.cross + i));
+        const int parts = x.z + 1;
+        if (parts <= kShort) continue;
+        Cols acc = n ? sum_parts(w, x, parts * warp / kEmbWarps, parts * (warp + 1) / kEmbWarps, c) : all(0.0f);
+        sums[warp][0][lane] = make_float4(acc.p[0].x, acc.p[0].y, acc.p[1].x, acc.p[1].y);
+        sums[warp][1][lane] = make_float4(acc.p[2].x, acc.p[2].y, acc.p[3].x, acc.p[3].y);
         __syncthreads();
         if (warp == 0) {
-            for (int q = 1; q < kEmbWarps; ++q)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) acc.set(e, acc.get(e) + part[q][lane * kGran + e]);
-            store_row<D>(a, row, g, acc, lane);
+            for (int q = 1; q < kEmbWarps; ++q) {
+                const float4 u = sums[q][0][lane], v = sums[q][1][lane];
+                acc = acc + Cols{{make_float2(u.x, u.y), make_float2(u.z, u.w), make_float2(v.x, v.y), make_float2(v.z, v.w)}};
+            }
+            store_row<D, kAligned>(a, x.x, g, acc, lane);
         }
         __syncthreads();
     }
+}
+
+template <typename S, typename D, bool kAligned>
+cudaError_t embedding_grad_as(const EmbeddingGradArgs& a, cudaStream_t s) {
+    const GradWork w = grad_work(a.work, a.n, a.vocab, a.cols, nullptr);
+    int need = 1;
+    while (((int64_t)1 << need) <= a.vocab) ++need;  // bits of the values 0 .. vocab
+    const bool few = a.n <= kFewTokens;
+    const int passes = few ? 1 : (need + kMaxBits - 1) / kMaxBits, bits = (need + passes - 1) / passes;
+    const int spans = (int)((a.cols + kSpan - 1) / kSpan);
+    const int64_t sums = (w.nchunks * (int64_t)spans + kEmbWarps - 1) / kEmbWarps;
+    // a warp of zeros takes one row, or more that make up 8 KB
+    int per = 1;
+    while (per < 32 && 2 * per * a.cols * (int64_t)sizeof(D) <= 8192) per *= 2;
+    const int64_t zeros = a.accumulate ? 0 : (a.vocab + per * kEmbWarps - 1) / (per * kEmbWarps);
+    const int ys = w.nchunks <= 1 ? 0 : (w.nchunks - 1 < 64 ? w.nchunks - 1 : 64);
+    if (sums > 0x7fffffff || zeros + (int64_t)spans * ys > 0x7fffffff) return cudaErrorInvalidValue;
+    cudaError_t e = cudaSuccess;
+    if (few && a.n > 0) {
+        embedding_few_kernel<<<1, kFewTokens, 0, s>>>(a, w);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        count_launch();
+    } else if (a.n > 0) {
+        const size_t smem = SortSmem::bytes(1 << bits);
+        if ((e = cudaFuncSetAttribute(embedding_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(a.n <= 4096 ? 1 : kSortCluster);
+        cfg.blockDim = dim3(kSortThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        cudaLaunchAttribute at;
+        at.id = cudaLaunchAttributeClusterDimension;
+        at.val.clusterDim.x = cfg.gridDim.x;
+        at.val.clusterDim.y = at.val.clusterDim.z = 1;
+        cfg.attrs = &at;
+        cfg.numAttrs = 1;
+        if ((e = cudaLaunchKernelEx(&cfg, embedding_sort_kernel, a, w, passes, bits)) != cudaSuccess) return e;
+        count_launch();
+    }
+    const int2* const sorted = w.sorted[(passes - 1) & 1];
+    if (a.n > 0) {
+        e = launch_next(embedding_sum_kernel<S, D, kAligned>, dim3((unsigned)sums), 32 * kEmbWarps, s, a, w, sorted, spans);
+        if (e != cudaSuccess) return e;
+        count_launch();
+    }
+    const dim3 grid((unsigned)(zeros + spans * ys));
+    if (grid.x == 0) return cudaSuccess;
+    if (a.n > 0) {
+        e = launch_next(embedding_join_kernel<D, kAligned>, grid, 32 * kEmbWarps, s, a, w, spans, ys, per);
+    } else {  // nothing before it, and so nothing for its zeros to run beside
+        embedding_join_kernel<D, kAligned><<<grid, 32 * kEmbWarps, 0, s>>>(a, w, spans, ys, per);
+        e = cudaGetLastError();
+    }
+    if (e == cudaSuccess) count_launch();
+    return e;
 }
 
 template <typename S, typename D>
 cudaError_t embedding_grad(const EmbeddingGradArgs& a, cudaStream_t s) {
-    const GradWork w = grad_work(a.work, a.n, a.cols, nullptr);
-    int need = 1;
-    while (((int64_t)1 << need) <= a.vocab) ++need;  // bits of the values 0 .. vocab
-    const int passes = (need + 7) / 8, bits = (need + passes - 1) / passes;
-    const int blocks = a.n <= 8192 ? 1 : kSortCluster;
-    const int64_t spans = (a.cols + kSpan - 1) / kSpan;
-    // one block of zeros per SM beside the sort
-    const int zeros = a.accumulate ? 0 : sm_count();
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(blocks + (zeros + blocks - 1) / blocks * blocks);
-    cfg.blockDim = dim3(kSortThreads);
-    cfg.dynamicSmemBytes = sizeof(SortSmem);
-    cfg.stream = s;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = blocks;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, embedding_sort_kernel<D>, a, w, blocks, passes, bits);
-    if (e != cudaSuccess) return e;
+    const bool aligned = a.cols % kGran == 0 && on_grid(a.grad, sizeof(S)) && on_grid(a.table, sizeof(D));
+    return aligned ? embedding_grad_as<S, D, true>(a, s) : embedding_grad_as<S, D, false>(a, s);
+}
+
+template <typename S, typename D>
+cudaError_t embedding(const EmbeddingArgs& a, cudaStream_t s) {
+    const int64_t spans = (a.cols + kSpan - 1) / kSpan, steps = (spans + kEmbSpans - 1) / kEmbSpans, items = steps * a.n;
+    const int per = (int)((spans + steps - 1) / steps);
+    const int64_t blocks = (items + kEmbWarps - 1) / kEmbWarps;
+    const unsigned grid = (unsigned)(blocks < 0x7fffffff ? blocks : 0x7fffffff);
+    const bool aligned = a.cols % kGran == 0 && on_grid(a.table, sizeof(S)) && on_grid(a.out, sizeof(D));
+    if (aligned)
+        embedding_kernel<S, D, true><<<grid, 32 * kEmbWarps, 0, s>>>(a, steps, per, items);
+    else
+        embedding_kernel<S, D, false><<<grid, 32 * kEmbWarps, 0, s>>>(a, steps, per, items);
     count_launch();
-    if (a.n == 0) return cudaSuccess;
-    const int *rows = w.rows[(passes - 1) & 1], *toks = w.toks[(passes - 1) & 1];
-    const int64_t items = w.nchunks * spans;
-    embedding_sum_kernel<S, D><<<(unsigned)((items + kEmbWarps - 1) / kEmbWarps), 32 * kEmbWarps, 0, s>>>(a, w, rows, toks, spans);
-    count_launch();
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if (w.nchunks > 1) {
-        const int64_t y = w.nchunks - 1 < 64 ? w.nchunks - 1 : 64;
-        embedding_join_kernel<D><<<dim3((unsigned)spans, (unsigned)y), 32 * kEmbWarps, 0, s>>>(a, w, rows);
-        count_launch();
-        e = cudaGetLastError();
-    }
-    return e;
+    return cudaGetLastError();
 }
 
 }  // namespace
 
 size_t embedding_grad_bytes(int64_t n, int64_t vocab, int64_t cols) {
     size_t bytes = 0;
-    grad_work(nullptr, n, cols, &bytes);
+    grad_work(nullptr, n, vocab, cols, &bytes);
     return bytes;
 }
 
 cudaError_t launch_embedding(int table_dt, int out_dt, const EmbeddingArgs& a, cudaStream_t s) {
     if (a.n == 0 || a.cols == 0) return cudaSuccess;
-    const int64_t spans = (a.cols + kSpan - 1) / kSpan, items = spans * a.n;
-    const int64_t blocks = (items + kEmbWarps - 1) / kEmbWarps;
-    const unsigned grid = (unsigned)(blocks < 0x7fffffff ? blocks : 0x7fffffff);
-    const int block = 32 * kEmbWarps;
-    if (table_dt == FSDP_F32 && out_dt == FSDP_F32)
-        embedding_kernel<float, float><<<grid, block, 0, s>>>(a, spans, items);
-    else if (table_dt == FSDP_F32)
-        embedding_kernel<float, uint16_t><<<grid, block, 0, s>>>(a, spans, items);
-    else if (out_dt == FSDP_F32)
-        embedding_kernel<uint16_t, float><<<grid, block, 0, s>>>(a, spans, items);
-    else
-        embedding_kernel<uint16_t, uint16_t><<<grid, block, 0, s>>>(a, spans, items);
-    count_launch();
-    return cudaGetLastError();
+    if (table_dt == FSDP_F32) return out_dt == FSDP_F32 ? embedding<float, float>(a, s) : embedding<float, uint16_t>(a, s);
+    return out_dt == FSDP_F32 ? embedding<uint16_t, float>(a, s) : embedding<uint16_t, uint16_t>(a, s);
 }
 
 cudaError_t launch_embedding_grad(int grad_dt, int table_dt, const EmbeddingGradArgs& a, cudaStream_t s) {

@@ -100,6 +100,7 @@ int check_aligned(const char* what, const char* name, const void* p, int es) {
 
 int launched(cudaError_t e, const char* what) {
     if (e == cudaSuccess) return FSDP_OK;
+    (void)cudaGetLastError();  // reported here, not by the caller's next call
     return set_error(FSDP_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
 }
 
