@@ -373,9 +373,11 @@ def _types():
     """torch dtypes of the operators' values and of their ids, as the C ABI's."""
     import torch
 
-    _TYPES.update({torch.float32: FSDP_F32, torch.bfloat16: FSDP_BF16})
     _TYPES["ids"] = {torch.int32: FSDP_I32, torch.int64: FSDP_I64}
     _TYPES["device"] = torch.cuda.current_device
+    # the current stream's handle without a Stream object around it (2.8 us a call)
+    _TYPES["stream"] = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    _TYPES.update({torch.float32: FSDP_F32, torch.bfloat16: FSDP_BF16})
     return _TYPES
 
 
@@ -414,9 +416,11 @@ def _like(what, name, t, rows, cols, dt, dev):
     return p, stride
 
 
-def _on(what, dev):
+def _on(what, dev, stream):
+    """The stream's handle; the tensors' device has to be the current one."""
     if dev != _TYPES["device"]():
         _refuse(what, f"the tensors are on cuda:{dev}, which is not the current device")
+    return _TYPES["stream"](dev) if stream is None else getattr(stream, "cuda_stream", stream)
 
 
 def _vector(what, name, t, n, dev, dtype=None):
@@ -460,8 +464,8 @@ def fsdp_embedding(table, ids, out, scale=1.0, first_row=0, stream=None):
     op, rows, ocols, os_, odt, odev = _matrix(what, "out", out)
     if n and (rows != n or ocols != cols) or odev != dev:
         _refuse(what, f"out is {rows} x {ocols} on cuda:{odev}; expected {n} x {cols} on cuda:{dev}")
-    _on(what, dev)
-    _check(lib().fsdp_embedding(tdt, tp, ts, vocab, cols, it, ip, n, first_row, scale, odt, op, os_, _stream(stream)))
+    handle = _on(what, dev, stream)
+    _check(lib().fsdp_embedding(tdt, tp, ts, vocab, cols, it, ip, n, first_row, scale, odt, op, os_, handle))
 
 
 def fsdp_embedding_grad_workspace(n_ids, vocab, cols):
@@ -483,9 +487,9 @@ def fsdp_embedding_grad(grad_out, ids, grad_table, workspace, scale=1.0, first_r
     if n and (rows != n or cols != tcols) or tdev != dev:
         _refuse(what, f"grad_out is {rows} x {cols}, ids {n}, grad_table {vocab} x {tcols} on cuda:{tdev}")
     wp, wb = _work(what, workspace, dev)
-    _on(what, dev)
+    handle = _on(what, dev, stream)
     _check(lib().fsdp_embedding_grad(gdt, gp, gs, it, ip, n, first_row, scale, int(accumulate), tdt, tp, ts, vocab,
-                                     tcols, wp, wb, _stream(stream)))
+                                     tcols, wp, wb, handle))
 
 
 def fsdp_dropout(x, out, p, seed, draw=0, residual=None, stream=None):
@@ -496,8 +500,8 @@ def fsdp_dropout(x, out, p, seed, draw=0, residual=None, stream=None):
     xp, rows, cols, xs, dt, dev = _matrix(what, "x", x)
     rp, rs = _like(what, "residual", residual, rows, cols, dt, dev)
     op, os_ = _like(what, "out", out, rows, cols, dt, dev)
-    _on(what, dev)
-    _check(lib().fsdp_dropout(rows, cols, dt, xp, xs, rp, rs, p, seed, draw, op, os_, _stream(stream)))
+    handle = _on(what, dev, stream)
+    _check(lib().fsdp_dropout(rows, cols, dt, xp, xs, rp, rs, p, seed, draw, op, os_, handle))
 
 
 def fsdp_layer_norm(x, weight, bias, out, mean, rstd, eps=1e-5, residual=None, hidden=None, p=0.0, seed=0, draw=0,
@@ -513,9 +517,9 @@ def fsdp_layer_norm(x, weight, bias, out, mean, rstd, eps=1e-5, residual=None, h
     wp, bp, pdt = _pair(what, ("weight", "bias"), weight, bias, cols, dev)
     mp, _ = _vector(what, "mean", mean, rows, dev, FSDP_F32)
     sp, _ = _vector(what, "rstd", rstd, rows, dev, FSDP_F32)
-    _on(what, dev)
+    handle = _on(what, dev, stream)
     _check(lib().fsdp_layer_norm(rows, cols, dt, xp, xs, rp, rs, p, seed, draw, pdt, wp, bp, eps, hp, hs, op, os_, mp,
-                                 sp, _stream(stream)))
+                                 sp, handle))
 
 
 def fsdp_layer_norm_grad_workspace(rows, cols):
@@ -544,7 +548,7 @@ def fsdp_layer_norm_grad(grad_out, hidden, mean, rstd, weight, grad_x, grad_weig
     wp, wdt = _vector(what, "weight", weight, cols, dev)
     dwp, dbp, gdt = _pair(what, ("grad_weight", "grad_bias"), grad_weight, grad_bias, cols, dev)
     kp, kb = _work(what, workspace, dev)
-    _on(what, dev)
+    handle = _on(what, dev, stream)
     _check(lib().fsdp_layer_norm_grad(rows, cols, dt, gp, gs, ap, as_, hp, hs, mp, sp, FSDP_F32 if wdt is None else wdt,
                                       wp, p, seed, draw, int(accumulate), rp, rs, xp, xs, gdt, dwp, dbp, kp, kb,
-                                      _stream(stream)))
+                                      handle))

@@ -585,7 +585,9 @@ cudaError_t embedding_grad_as(const EmbeddingGradArgs& a, cudaStream_t s) {
         count_launch();
     } else if (a.n > 0) {
         const size_t smem = SortSmem::bytes(1 << bits);
-        if ((e = cudaFuncSetAttribute(embedding_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
+        static std::atomic<uint64_t> done{0};
+        e = allow_smem(reinterpret_cast<const void*>(embedding_sort_kernel), (int)SortSmem::bytes(1 << kMaxBits), done);
+        if (e != cudaSuccess) return e;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(a.n <= 4096 ? 1 : kSortCluster);
         cfg.blockDim = dim3(kSortThreads);

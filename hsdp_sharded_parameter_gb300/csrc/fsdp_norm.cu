@@ -546,7 +546,8 @@ Shape norm_shape(int64_t rows, int64_t cols, int streams, int slot_bytes) {
 template <typename T, int V, bool kAligned, int kMode>
 cudaError_t norm_rows(const NormArgs& a, const Shape& f, cudaStream_t s) {
     auto kernel = norm_kernel<T, V, kAligned, kMode>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)f.smem);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), (int)kSmemMost, done);
     if (e != cudaSuccess) return e;
     kernel<<<(unsigned)f.grid, 32 * f.gw * f.groups, f.smem, s>>>(a, f.gw, f.depth);
     return cudaGetLastError();
@@ -604,7 +605,8 @@ Shape grad_shape(int64_t rows, int64_t cols, int streams, int slot_bytes) {
 template <typename T, int V, bool kAligned, int kMode>
 cudaError_t grad_rows(const NormGradArgs& a, const Shape& f, int64_t stride, cudaStream_t s) {
     auto kernel = norm_grad_kernel<T, V, kAligned, kMode>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)f.smem);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), (int)kSmemMost, done);
     if (e != cudaSuccess) return e;
     kernel<<<(unsigned)f.grid, 32 * f.gw * f.groups, f.smem, s>>>(a, f.gw, f.depth, stride);
     return cudaGetLastError();

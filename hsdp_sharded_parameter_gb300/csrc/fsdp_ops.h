@@ -5,6 +5,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -80,6 +81,9 @@ struct NormGradArgs {
 
 // SMs of the current device.
 int sm_count();
+// Lets a kernel take up to `bytes` of dynamic shared memory on the current
+// device; `done` remembers the devices it was said for.
+cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done);
 
 size_t embedding_grad_bytes(int64_t n, int64_t vocab, int64_t cols);
 size_t norm_grad_bytes(int64_t rows, int64_t cols);
