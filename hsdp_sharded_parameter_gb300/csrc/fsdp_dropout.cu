@@ -12,27 +12,48 @@ template <typename T>
 constexpr int kDropSpans = sizeof(T) == 4 ? 2 : 4;
 
 // A warp takes kU neighbouring spans of 256 columns of a row at a time and
-// loads them all before it draws the first mask.
+// starts all their loads before it draws the first mask: into registers, or,
+// for rows off the 16-byte grid, whose granules are put together from two
+// blocks each, into shared memory (kept in registers, they left room for half
+// the loads in flight).
 template <typename T, bool kAligned>
 __global__ void __launch_bounds__(32 * kDropWarps, 4) dropout_kernel(DropoutArgs a, int64_t steps, int64_t items) {
     constexpr int kU = kDropSpans<T>;
+    __shared__ uint4 staged[kAligned ? 1 : kDropWarps][kAligned ? 1 : 2 * kU][kAligned ? 1 : kSlot<false, T>];
     const int lane = threadIdx.x & 31;
+    uint4(*const mine)[kAligned ? 1 : kSlot<false, T>] = staged[kAligned ? 0 : threadIdx.x >> 5];
     for (int64_t it = warp_id(); it < items; it += warp_count()) {
-        const int64_t row = it / steps, g0 = (it - row * steps) * (kU * 32) + lane;
+        const int64_t row = it / steps, g0 = (it - row * steps) * (kU * 32) + lane, c0 = (g0 - lane) * kGran;
         const T* x = static_cast<const T*>(a.x.data) + row * a.x.stride;
         const T* res = static_cast<const T*>(a.res.data) + row * a.res.stride;
         T* out = static_cast<T*>(a.out.data) + row * a.out.stride;
+        const int left = (int)(a.cols - c0 < kU * kSpan ? a.cols - c0 : kU * kSpan);
         Raw<T> in[kU], add[kU];
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-            const int64_t g = g0 + u * 32;
-            const int n = granule_cols(g, a.cols);
-            load_cols<kAligned>(in[u], x, g * kGran, n);
-            if (a.res.data) load_cols<kAligned>(add[u], res, g * kGran, n);
+            if constexpr (kAligned) {
+                const int64_t g = g0 + u * 32;
+                const int n = granule_cols(g, a.cols);
+                load_cols<true>(in[u], x, g * kGran, n);
+                if (a.res.data) load_cols<true>(add[u], res, g * kGran, n);
+            } else {
+                span_fetch<false>(mine[u], x + c0, u * kSpan, left, lane);
+                if (a.res.data) span_fetch<false>(mine[kU + u], res + c0, u * kSpan, left, lane);
+            }
+        }
+        if constexpr (!kAligned) {
+            async_commit();
+            async_wait<0>();
+            __syncwarp();
         }
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
             const int64_t g = g0 + u * 32;
+            if constexpr (!kAligned) {
+                if (u * kSpan >= left) break;
+                span_read<false>(in[u], mine[u], x + c0, u * kSpan, lane);
+                if (a.res.data) span_read<false>(add[u], mine[kU + u], res + c0, u * kSpan, lane);
+            }
             const Cols v = widened(in[u]);
             Cols y = a.res.data ? widened(add[u]) : all(0.0f);
             if (a.mask.drops)
@@ -42,6 +63,7 @@ __global__ void __launch_bounds__(32 * kDropWarps, 4) dropout_kernel(DropoutArgs
             round_to(y, in[u]);
             store_cols<kAligned>(out + g * kGran, in[u], granule_cols(g, a.cols), lane);
         }
+        if constexpr (!kAligned) __syncwarp();  // before the next spans come in
     }
 }
 

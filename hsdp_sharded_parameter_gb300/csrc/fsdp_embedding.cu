@@ -36,27 +36,42 @@ constexpr int kEmbSpans = 4;
 
 template <typename S, typename D, bool kAligned>
 __global__ void __launch_bounds__(32 * kEmbWarps) embedding_kernel(EmbeddingArgs a, int64_t steps, int per, int64_t items) {
+    // rows off the 16-byte grid come in through shared memory
+    __shared__ uint4 staged[kAligned ? 1 : kEmbWarps][kAligned ? 1 : kEmbSpans][kAligned ? 1 : kSlot<false, S>];
     const int lane = threadIdx.x & 31;
+    uint4(*const mine)[kAligned ? 1 : kSlot<false, S>] = staged[kAligned ? 0 : threadIdx.x >> 5];
     for (int64_t it = warp_id(); it < items; it += warp_count()) {
-        const int64_t t = it / steps, g0 = (it - t * steps) * (per * 32) + lane;
+        const int64_t t = it / steps, g0 = (it - t * steps) * (per * 32) + lane, c0 = (g0 - lane) * kGran;
         const int64_t row = row_of(read_id(a.ids, a.wide_ids, t), a.first, a.vocab);
         const bool named = row < a.vocab;
         const S* from = static_cast<const S*>(a.table.data) + row * a.table.stride;
         D* to = static_cast<D*>(a.out.data) + t * a.out.stride;
+        const int left = (int)(a.cols - c0 < per * kSpan ? a.cols - c0 : per * kSpan);
         Raw<S> in[kEmbSpans];
 #pragma unroll
         for (int u = 0; u < kEmbSpans; ++u) {
-            const int64_t g = g0 + u * 32;
-            if (named && u < per) load_cols<kAligned>(in[u], from, g * kGran, granule_cols(g, a.cols));
+            if (!named || u >= per) break;
+            if constexpr (kAligned)
+                load_cols<true>(in[u], from, (g0 + u * 32) * kGran, granule_cols(g0 + u * 32, a.cols));
+            else
+                span_fetch<false>(mine[u], from + c0, u * kSpan, left, lane);
+        }
+        if constexpr (!kAligned) {
+            async_commit();
+            async_wait<0>();
+            __syncwarp();
         }
 #pragma unroll
         for (int u = 0; u < kEmbSpans; ++u) {
-            if (u >= per) break;
+            if (u * kSpan >= left) break;
             const int64_t g = g0 + u * 32;
+            if constexpr (!kAligned)
+                if (named) span_read<false>(in[u], mine[u], from + c0, u * kSpan, lane);
             Raw<D> r;
             round_to(named ? widened(in[u]) * all(a.scale) : all(0.0f), r);
             store_cols<kAligned>(to + g * kGran, r, granule_cols(g, a.cols), lane);
         }
+        if constexpr (!kAligned) __syncwarp();  // before the next spans come in
     }
 }
 
@@ -418,7 +433,10 @@ __device__ __forceinline__ void list_crossing(const GradWork& w, const int2* sor
         hi = lo + (int)(more + 1) * gap < hi ? lo + (int)(more + 1) * gap : hi;
         lo += (int)more * gap;
     }
-    if (lane == 0) w.cross[atomicAdd(w.crossings, 1)] = Crossing{row, chunk, lo - chunk, 0};
+    if (lane == 0) {
+        const int at = atomicAdd(w.crossings, 1);
+        if (at < w.nchunks) w.cross[at] = Crossing{row, chunk, lo - chunk, 0};
+    }
 }
 
 // Zeros for a row of n elements, by one warp.
@@ -450,55 +468,66 @@ __device__ __forceinline__ void write_zeros(const EmbeddingGradArgs& a, const ui
         if (!(named >> i & 1)) zero_row(static_cast<D*>(a.table.data) + (r0 + i) * a.table.stride, a.cols, lane);
 }
 
-// Tokens whose gradients a lane has in flight.
-template <typename S>
-constexpr int kFlight = sizeof(S) == 4 ? 4 : 8;
+// Tokens whose gradients a warp has in flight, in shared memory.
+constexpr int kFlight = 8;
 
 template <typename S, typename D, bool kAligned>
-__global__ void __launch_bounds__(32 * kEmbWarps, 3)
+__global__ void __launch_bounds__(32 * kEmbWarps, sizeof(S) == 4 ? 3 : 5)
     embedding_sum_kernel(EmbeddingGradArgs a, GradWork w, const int2* sorted, int spans) {
-    constexpr int kU = kFlight<S>;
+    extern __shared__ uint4 flight[];
+    constexpr int kOne = kSlot<kAligned, S>;
+    uint4* const slots = flight + (threadIdx.x >> 5) * kFlight * kOne;
     const int lane = threadIdx.x & 31;
     const int64_t it = warp_id();
     const int64_t chunk = it / spans;
     const int g = (int)(it - chunk * spans) * 32 + lane, n = granule_cols((int64_t)g, a.cols);
-    const int64_t c = (int64_t)g * kGran;
+    const int64_t c = (int64_t)g * kGran, c0 = c - lane * kGran;
+    const int left = (int)(a.cols - c0 < kSpan ? a.cols - c0 : kSpan);
     wait_for_previous();
     allow_next();  // not before: the next kernel's zeros need the sort's marks
-    const int count = __ldcg(w.count);
+    const int count = min(__ldcg(w.count), (int)a.n);
     if (chunk * w.chunk >= count) return;
     const int lo = (int)chunk * w.chunk, m = count - lo < w.chunk ? count - lo : w.chunk;
-    const int2 mine = lane < m ? __ldcg(sorted + lo + lane) : make_int2(-1, 0);
+    // (calls that shared a workspace in spite of the header would leave any
+    // numbers there: no gradient, row or part outside its matrix is touched)
+    int2 mine = lane < m ? __ldcg(sorted + lo + lane) : make_int2(-1, 0);
+    mine = make_int2(min(mine.x, (int)a.vocab - 1), (int)min((unsigned)mine.y, (unsigned)a.n - 1));
     const int prev = lo > 0 ? __ldcg(&sorted[lo - 1].x) : -1;
     const int next = lo + m < count ? __ldcg(&sorted[lo + m].x) : -1;
+    auto gradient = [&](int j) {
+        return static_cast<const S*>(a.grad.data) + (int64_t)__shfl_sync(kFull, mine.y, j & 31) * a.grad.stride + c0;
+    };
+    auto fetch = [&](int j) {
+        const S* from = gradient(j);
+        if (j < m) span_fetch<kAligned>(slots + j % kFlight * kOne, from, 0, left, lane);
+        async_commit();
+    };
     Cols acc = all(0.0f);
     int cur = -1;
     bool open = false;  // cur began in an earlier chunk
-    for (int j = 0; j < m; j += kU) {
-        Raw<S> in[kU];
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int64_t t = __shfl_sync(kFull, mine.y, (j + u) & 31);
-            if (j + u < m) load_cols<kAligned>(in[u], static_cast<const S*>(a.grad.data) + t * a.grad.stride, c, n);
-        }
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int row = __shfl_sync(kFull, mine.x, (j + u) & 31);
-            if (j + u >= m) break;
-            if (row != cur) {
-                if (cur >= 0) {
-                    if (!open)
-                        store_row<D, kAligned>(a, cur, g, acc, lane);
-                    else if (n)
-                        store_part(w.part + chunk * w.stride + c, acc);
-                }
-                open = cur < 0 && row == prev;
-                cur = row;
-                acc = widened(in[u]);
-            } else {
-                acc = acc + widened(in[u]);
+    for (int j = 0; j < kFlight - 1; ++j) fetch(j);
+#pragma unroll 1
+    for (int j = 0; j < m; ++j) {
+        fetch(j + kFlight - 1);
+        async_wait<kFlight - 1>();
+        __syncwarp();
+        Raw<S> in;
+        span_read<kAligned>(in, slots + j % kFlight * kOne, gradient(j), 0, lane);
+        const int row = __shfl_sync(kFull, mine.x, j);
+        if (row != cur) {
+            if (cur >= 0) {
+                if (!open)
+                    store_row<D, kAligned>(a, cur, g, acc, lane);
+                else if (n)
+                    store_part(w.part + chunk * w.stride + c, acc);
             }
+            open = cur < 0 && row == prev;
+            cur = row;
+            acc = widened(in);
+        } else {
+            acc = acc + widened(in);
         }
+        __syncwarp();  // before the slot is filled again
     }
     if (open) {
         if (n) store_part(w.part + chunk * w.stride + c, acc);
@@ -517,6 +546,10 @@ __device__ __forceinline__ Cols sum_parts(const GradWork& w, const int4& x, int 
 #pragma unroll 4
     for (int p = p0; p < p1; ++p) acc = acc + load_part(w.part + (x.y + p + (p == 0 ? w.nchunks : 0)) * w.stride + c);
     return acc;
+}
+
+__device__ __forceinline__ bool sound(const EmbeddingGradArgs& a, const GradWork& w, const int4& x) {
+    return (unsigned)x.x < (unsigned)a.vocab && (unsigned)x.y < (unsigned)w.nchunks && (unsigned)x.z < (unsigned)(w.nchunks - x.y);
 }
 
 // The first spans * y blocks, block (span, y): the rows that cross chunks, for
@@ -538,16 +571,16 @@ __global__ void __launch_bounds__(32 * kEmbWarps) embedding_join_kernel(Embeddin
     const int64_t g = (int64_t)(blockIdx.x - y * spans) * 32 + lane, c = g * kGran;
     const int n = granule_cols(g, a.cols);
     wait_for_previous();
-    const int crossings = __ldcg(w.crossings);
+    const int crossings = min(__ldcg(w.crossings), w.nchunks);
     for (int i = y * kEmbWarps + warp; i < crossings; i += ys * kEmbWarps) {
         const int4 x = __ldcg(reinterpret_cast<const int4*>(w.cross + i));
-        if (x.z >= kShort) continue;
+        if (x.z >= kShort || !sound(a, w, x)) continue;
         store_row<D, kAligned>(a, x.x, g, n ? sum_parts(w, x, 0, x.z + 1, c) : all(0.0f), lane);
     }
     for (int i = y; i < crossings; i += ys) {
         const int4 x = __ldcg(reinterpret_cast<const int4*>(w.cross + i));
         const int parts = x.z + 1;
-        if (parts <= kShort) continue;
+        if (parts <= kShort || !sound(a, w, x)) continue;
         Cols acc = n ? sum_parts(w, x, parts * warp / kEmbWarps, parts * (warp + 1) / kEmbWarps, c) : all(0.0f);
         sums[warp][0][lane] = make_float4(acc.p[0].x, acc.p[0].y, acc.p[1].x, acc.p[1].y);
         sums[warp][1][lane] = make_float4(acc.p[2].x, acc.p[2].y, acc.p[3].x, acc.p[3].y);
@@ -604,14 +637,18 @@ cudaError_t embedding_grad_as(const EmbeddingGradArgs& a, cudaStream_t s) {
     }
     const int2* const sorted = w.sorted[(passes - 1) & 1];
     if (a.n > 0) {
-        e = launch_next(embedding_sum_kernel<S, D, kAligned>, dim3((unsigned)sums), 32 * kEmbWarps, s, a, w, sorted, spans);
+        constexpr int smem = kEmbWarps * kFlight * kSlot<kAligned, S> * 16;
+        static std::atomic<uint64_t> done{0};
+        auto kernel = embedding_sum_kernel<S, D, kAligned>;
+        if ((e = allow_smem(reinterpret_cast<const void*>(kernel), smem, done)) != cudaSuccess) return e;
+        e = launch_next(kernel, dim3((unsigned)sums), 32 * kEmbWarps, smem, s, a, w, sorted, spans);
         if (e != cudaSuccess) return e;
         count_launch();
     }
     const dim3 grid((unsigned)(zeros + spans * ys));
     if (grid.x == 0) return cudaSuccess;
     if (a.n > 0) {
-        e = launch_next(embedding_join_kernel<D, kAligned>, grid, 32 * kEmbWarps, s, a, w, spans, ys, per);
+        e = launch_next(embedding_join_kernel<D, kAligned>, grid, 32 * kEmbWarps, 0, s, a, w, spans, ys, per);
     } else {  // nothing before it, and so nothing for its zeros to run beside
         embedding_join_kernel<D, kAligned><<<grid, 32 * kEmbWarps, 0, s>>>(a, w, spans, ys, per);
         e = cudaGetLastError();

@@ -17,6 +17,18 @@
 // depend on how many warps fit beside the row's registers.
 #include "fsdp_ops.cuh"
 
+#ifndef TW
+#define TW 3
+#endif
+#ifndef TV
+#define TV 1
+#endif
+#ifndef TX
+#define TX 32
+#endif
+#ifndef TS
+#define TS 200
+#endif
 namespace fsdp {
 namespace {
 
@@ -268,11 +280,37 @@ __device__ __forceinline__ void store_grad(const NormGradArgs& a, const Cols& t,
     store_cols<kAligned>(grad_x + g * kGran, r, n, lane);
 }
 
-// parts[block][0 weight, 1 bias][stride]: the sums of a block's rows.
+// Two sums of a row over its group's warps, in two steps with one barrier of
+// the block between them. Lanes 0 to 15 work on the first value, the others on
+// the second.
+__device__ __forceinline__ float pair_begin(float a, float b, int lane, float* part) {
+    float v = lane < 16 ? a : b;
+    v += __shfl_xor_sync(kFull, lane < 16 ? b : a, 16);
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
+    if ((lane & 15) == 0) part[lane] = v;  // lane 0: the first sum, lane 16: the second
+    return v;
+}
+__device__ __forceinline__ float2 pair_end(float v, int gw, int lane, const float* part) {
+    if (gw > 1) {
+        v = (lane & 15) < gw ? part[(lane & 15) * 32 + (lane & 16)] : 0.0f;
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
+    }
+    return make_float2(__shfl_sync(kFull, v, 0), __shfl_sync(kFull, v, 16));
+}
+
+// parts[block][0 weight, 1 bias][stride]: the sums of a block's rows. A row is
+// read twice from shared memory: for its two sums, and, an iteration later,
+// for its gradient. One barrier an iteration, and between two of them the one
+// row's gradient and the next one's sums, which do not depend on each other:
+// with the gradient right behind its sums, the 16 warps that the columns'
+// sums leave room for waited for each other (8192 columns: 327 us, now 250).
 template <typename T, int V, bool kAligned, int kMode>
-__global__ void __launch_bounds__(V == 1 ? 128 : 512, V == 1 ? 8 : 1)
+__global__ void __launch_bounds__(V == 1 ? 256 : 512, V == 1 ? TW : 1)
     norm_grad_kernel(NormGradArgs a, int gw, int depth, int64_t stride) {
     extern __shared__ uint4 ring[];
+    __shared__ float part[2][kWarps * 32];
     allow_next();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, group = w / gw, warp = w - group * gw;
     const int groups = (blockDim.x >> 5) / gw, streams = has<kMode>(kResidual, a.grad_hidden.data) ? 3 : 2;
@@ -281,6 +319,7 @@ __global__ void __launch_bounds__(V == 1 ? 128 : 512, V == 1 ? 8 : 1)
     const uint32_t as = (uint32_t)a.grad_hidden.stride * sizeof(T);
     const uint32_t rs = (uint32_t)a.grad_res.stride * sizeof(T), xs = (uint32_t)a.grad_x.stride * sizeof(T);
     constexpr int kOne = kSlot<kAligned, T>;
+    constexpr bool kHold = V <= 2;  // the weight in registers
     uint4* const mine = ring + (size_t)w * depth * streams * V * kOne;
     const int cols = (int)a.cols;
     const float inv = 1.0f / (float)cols;
@@ -302,73 +341,101 @@ __global__ void __launch_bounds__(V == 1 ? 128 : 512, V == 1 ? 8 : 1)
         async_commit();
     };
 
-    Cols dw[V], db[V];
+    Cols dw[V], db[V], held[kHold ? V : 1];
 #pragma unroll
-    for (int v = 0; v < V; ++v) dw[v] = db[v] = all(0.0f);
-    uint32_t row = blockIdx.x * groups + group;
-    for (int d = 0; d + 1 < depth; ++d) fetch(row + d * step, d);
-    // a row's mean and rstd are loaded a row ahead
-    float next_mean = row < rows ? __ldg(a.mean + row) : 0.0f, next_rstd = row < rows ? __ldg(a.rstd + row) : 0.0f;
-    int slot = 0, side = 0;
-    for (uint32_t r0 = blockIdx.x * groups; r0 < rows; r0 += step, row += step) {
-        __syncwarp();
-        fetch(row + (depth - 1) * step, slot == 0 ? depth - 1 : slot - 1);
-        const float mean = next_mean, rstd = next_rstd;
-        if (row + step < rows) {
-            next_mean = __ldg(a.mean + row + step);
-            next_rstd = __ldg(a.rstd + row + step);
+    for (int v = 0; v < V; ++v) {
+        const int g = (v * gw + warp) * 32 + lane;
+        dw[v] = db[v] = all(0.0f);
+        if (kHold) held[kHold ? v : 0] = load_param<kAligned>(a.weight, a.param_dt, g * kGran, granule_cols(g, cols), 1.0f);
+    }
+    auto weight = [&](int v, int g, int n) {
+        return kHold ? held[kHold ? v : 0] : load_param<kAligned>(a.weight, a.param_dt, g * kGran, n, 1.0f);
+    };
+    // grad_out and u of a granule of a row that has arrived
+    auto read = [&](int v, int slot, uint32_t row, float mean, float rstd, int n, Cols& dy, Cols& u) {
+        const int c0 = (v * gw + warp) * kSpan;
+        const uint4* from = mine + slot * streams * V * kOne;
+        Raw<T> r, q;
+        span_read<kAligned>(r, from + v * kOne, row_at<const T>(a.grad.data, row, gs), c0, lane);
+        span_read<kAligned>(q, from + (V + v) * kOne, row_at<const T>(a.hidden.data, row, hs), c0, lane);
+        dy = widened(r);
+        u = (widened(q) + all(-mean)) * all(rstd);
+        if (!kAligned) {
+            cut(dy, n);
+            cut(u, n);
         }
-        async_wait_but(depth - 1);
-        __syncwarp();
-        const bool on = row < rows;
-        const T* dyp = row_at<const T>(a.grad.data, row, gs);
-        const T* hp = row_at<const T>(a.hidden.data, row, hs);
-        const T* past = row_at<const T>(a.grad_hidden.data, row, as);
-        const uint4* const from = mine + slot * streams * V * kOne;
-        Cols u[V], gr[V];
+    };
+    auto sums = [&](uint32_t row, int slot, float mean, float rstd, float* to) {
         float2 s1 = both(0.0f), s2 = both(0.0f);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int g = (v * gw + warp) * 32 + lane, c0 = (v * gw + warp) * kSpan;
-            const int n = on ? granule_cols(g, cols) : 0;
-            Raw<T> r, q;
-            span_read<kAligned>(r, from + v * kOne, dyp, c0, lane);
-            span_read<kAligned>(q, from + (V + v) * kOne, hp, c0, lane);
-            Cols dy = widened(r);
-            u[v] = (widened(q) + all(-mean)) * all(rstd);
-            if (!kAligned) {
-                cut(dy, n);
-                cut(u[v], n);
-            }
-            if (!kAligned || n) {
-                gr[v] = dy * load_param<kAligned>(a.weight, a.param_dt, g * kGran, n, 1.0f);
-                db[v] = db[v] + dy;
-                dw[v] = fma(dy, u[v], dw[v]);
-                sum_into(s1, gr[v]);
-                dot_into(s2, gr[v], u[v]);
-            }
-        }
-        float c[2] = {s1.x + s1.y, s2.x + s2.y};
-        group_sum(c, gw, group, warp, lane, side);
-        side ^= 1;
-        if (on) {
-            const Cols k0 = all(rstd), k1 = all(-(c[0] * inv)), k2 = all(-(c[1] * inv));
+        if (row < rows)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const int g = (v * gw + warp) * 32 + lane, c0 = (v * gw + warp) * kSpan;
-                const int n = granule_cols(g, cols);
-                Cols t = fma(u[v], k2, gr[v] + k1);
+                const int g = (v * gw + warp) * 32 + lane, n = granule_cols(g, cols);
+                Cols dy, u;
+                read(v, slot, row, mean, rstd, n, dy, u);
+                if (kAligned && !n) continue;
+                const Cols gr = dy * weight(v, g, n);
+                sum_into(s1, gr);
+                dot_into(s2, gr, u);
+            }
+        return pair_begin(s1.x + s1.y, s2.x + s2.y, lane, to);
+    };
+
+    uint32_t row = blockIdx.x * groups + group;
+    for (int d = 0; d + 1 < depth; ++d) fetch(row + d * step, d);
+    float mean = row < rows ? __ldg(a.mean + row) : 0.0f, rstd = row < rows ? __ldg(a.rstd + row) : 0.0f;
+    // a row's mean and rstd are loaded a row ahead
+    float next_mean = row + step < rows ? __ldg(a.mean + row + step) : 0.0f;
+    float next_rstd = row + step < rows ? __ldg(a.rstd + row + step) : 0.0f;
+    async_wait_but(depth - 2);
+    __syncwarp();
+    float sum = sums(row, 0, mean, rstd, &part[0][w * 32]);
+    int slot = 0, side = 0;
+    // every group of a block goes round as often, for the barriers
+    for (uint32_t r0 = blockIdx.x * groups; r0 < rows; r0 += step, row += step) {
+        __syncwarp();  // the last reads of the slot that is filled now
+        fetch(row + (depth - 1) * step, slot == 0 ? depth - 1 : slot - 1);
+        async_wait_but(depth - 2);
+        if (gw > 1)
+            __syncthreads();
+        else
+            __syncwarp();
+        const float2 c = pair_end(sum, gw, lane, &part[side][group * gw * 32]);
+        const int after = slot + 1 == depth ? 0 : slot + 1;
+        float m = 0.0f, r = 0.0f;
+        if (row + 2 * step < rows) {
+            m = __ldg(a.mean + row + 2 * step);
+            r = __ldg(a.rstd + row + 2 * step);
+        }
+        sum = sums(row + step, after, next_mean, next_rstd, &part[side ^ 1][w * 32]);
+        if (row < rows) {
+            const Cols k0 = all(rstd), k1 = all(-(c.x * inv)), k2 = all(-(c.y * inv));
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int g = (v * gw + warp) * 32 + lane, c0 = (v * gw + warp) * kSpan, n = granule_cols(g, cols);
+                Cols dy, u;
+                read(v, slot, row, mean, rstd, n, dy, u);
+                if (!kAligned || n) {
+                    db[v] = db[v] + dy;
+                    dw[v] = fma(dy, u, dw[v]);
+                }
+                Cols t = fma(u, k2, fma(dy, weight(v, g, n), k1));
                 if (has<kMode>(kResidual, a.grad_hidden.data)) {
-                    Raw<T> r;
-                    span_read<kAligned>(r, from + (2 * V + v) * kOne, past, c0, lane);
-                    t = fma(t, k0, widened(r));
+                    Raw<T> q;
+                    span_read<kAligned>(q, mine + (slot * streams * V + 2 * V + v) * kOne, row_at<const T>(a.grad_hidden.data, row, as), c0, lane);
+                    t = fma(t, k0, widened(q));
                 } else {
                     t = t * k0;
                 }
                 store_grad<kAligned, kMode>(a, t, row, g, n, lane, row_at<T>(a.grad_res.data, row, rs), row_at<T>(a.grad_x.data, row, xs));
             }
         }
-        slot = slot + 1 == depth ? 0 : slot + 1;
+        mean = next_mean;
+        rstd = next_rstd;
+        next_mean = m;
+        next_rstd = r;
+        slot = after;
+        side ^= 1;
     }
     // the block's groups, added in turn
     float4* const box = reinterpret_cast<float4*>(ring);
@@ -510,7 +577,7 @@ bool fits_32(const Mat& m, int es) { return m.stride < ((int64_t)1 << 32) / es; 
 
 // What the blocks of an SM may take of shared memory together: the rest of
 // its 256 KB is the L1 cache, where the parameters stay.
-constexpr int64_t kSmemPerSm = 132 * 1024, kSmemMost = 200 * 1024;
+constexpr int64_t kSmemPerSm = 132 * 1024, kSmemMost = TS * 1024;
 
 // How a kernel is launched on rows of these columns: V granules a thread, gw
 // warps a row, groups of them in a block, blocks of an SM, and the rows that
@@ -582,20 +649,21 @@ cudaError_t norm(const NormArgs& a, cudaStream_t s) {
 Shape grad_shape(int64_t rows, int64_t cols, int streams, int slot_bytes) {
     Shape f;
     const int64_t grans = (cols + kGran - 1) / kGran;
-    f.v = grans <= 32 * 4 ? 1 : (grans <= 32 * 32 ? 2 : 4);
+    f.v = grans <= 32 * TV ? 1 : (grans <= 32 * TX ? 2 : 4);
     f.gw = (int)((grans + 32 * f.v - 1) / (32 * f.v));
     f.groups = f.gw >= 4 ? 1 : 4 / f.gw;
     const int block = 32 * f.gw * f.groups;
-    f.per_sm = (f.v == 1 ? 1024 : 512) / block;
+    f.per_sm = (f.v == 1 ? 256 * TW : 512) / block;
     if (f.per_sm < 1) f.per_sm = 1;
     const int64_t need = (rows + f.groups - 1) / f.groups;
     const int64_t most = (int64_t)sm_count() * f.per_sm;
     f.grid = (int)(need < most ? need : most);
     const int64_t stage = (int64_t)f.gw * f.groups * f.v * slot_bytes * streams;
+    // two rows at least: a row's gradient beside the next one's sums
     int64_t depth = kSmemMost / f.per_sm / stage;
     if (depth > 4) depth = 4;
     if (depth > (need + f.grid - 1) / f.grid) depth = (need + f.grid - 1) / f.grid;
-    f.depth = (int)(depth > 1 ? depth : 1);
+    f.depth = (int)(depth > 2 ? depth : 2);
     f.smem = stage * f.depth;
     const int64_t box = f.groups > 1 ? (int64_t)f.gw * f.v * 2048 : 0;  // where the groups meet
     if (f.smem < box) f.smem = box;
@@ -625,8 +693,13 @@ template <typename T>
 cudaError_t norm_grad(const NormGradArgs& a, int* parts, cudaStream_t s) {
     const int es = (int)sizeof(T);
     const int64_t stride = grad_stride(a.cols);
-    if (a.cols > kNormCols || !fits_32(a.grad, es) || !fits_32(a.hidden, es) || !fits_32(a.grad_hidden, es) ||
-        !fits_32(a.grad_res, es) || !fits_32(a.grad_x, es)) {
+    const bool aligned = a.cols % kGran == 0 && on_grid(a.grad, es) && on_grid(a.hidden, es) && on_grid(a.grad_hidden, es) &&
+                         on_grid(a.grad_res, es) && on_grid(a.grad_x, es) && on_grid(Mat{const_cast<void*>(a.weight), 0}, es);
+    const int mode = (a.grad_hidden.data ? kResidual : 0) | (a.mask.drops ? kDrops : 0);
+    const Shape f = grad_shape(a.rows, a.cols, a.grad_hidden.data ? 3 : 2, 16 * (aligned ? kSlot<true, T> : kSlot<false, T>));
+    // fp32 rows of more than about 8192 columns do not fit shared memory twice
+    if (a.cols > kNormCols || f.smem > kSmemMost || !fits_32(a.grad, es) || !fits_32(a.hidden, es) ||
+        !fits_32(a.grad_hidden, es) || !fits_32(a.grad_res, es) || !fits_32(a.grad_x, es)) {
         norm_grad_wide_kernel<T><<<(unsigned)a.rows, kWideThreads, 0, s>>>(a);
         count_launch();
         *parts = (int)(a.rows < kWideParts ? a.rows : kWideParts);
@@ -634,10 +707,6 @@ cudaError_t norm_grad(const NormGradArgs& a, int* parts, cudaStream_t s) {
         count_launch();
         return cudaGetLastError();
     }
-    const bool aligned = a.cols % kGran == 0 && on_grid(a.grad, es) && on_grid(a.hidden, es) && on_grid(a.grad_hidden, es) &&
-                         on_grid(a.grad_res, es) && on_grid(a.grad_x, es) && on_grid(Mat{const_cast<void*>(a.weight), 0}, es);
-    const int mode = (a.grad_hidden.data ? kResidual : 0) | (a.mask.drops ? kDrops : 0);
-    const Shape f = grad_shape(a.rows, a.cols, a.grad_hidden.data ? 3 : 2, 16 * (aligned ? kSlot<true, T> : kSlot<false, T>));
     *parts = f.grid;
     count_launch();
     if (!aligned) return grad_v<T, false, kEither>(a, f, stride, s);
@@ -680,9 +749,9 @@ cudaError_t launch_norm_grad(int dt, int param_grad_dt, const NormGradArgs& a, c
     const int64_t stride = grad_stride(a.cols);
     count_launch();
     if (param_grad_dt == FSDP_F32)
-        return launch_next(norm_join_kernel<float>, grid, 32 * kJoinWarps, s, work, stride, parts, a.cols, a.accumulate,
+        return launch_next(norm_join_kernel<float>, grid, 32 * kJoinWarps, 0, s, work, stride, parts, a.cols, a.accumulate,
                            static_cast<float*>(a.grad_weight), static_cast<float*>(a.grad_bias));
-    return launch_next(norm_join_kernel<uint16_t>, grid, 32 * kJoinWarps, s, work, stride, parts, a.cols, a.accumulate,
+    return launch_next(norm_join_kernel<uint16_t>, grid, 32 * kJoinWarps, 0, s, work, stride, parts, a.cols, a.accumulate,
                        static_cast<uint16_t*>(a.grad_weight), static_cast<uint16_t*>(a.grad_bias));
 }
 

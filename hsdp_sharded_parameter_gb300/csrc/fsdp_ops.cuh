@@ -22,13 +22,44 @@ struct ElemOf<FSDP_BF16> {
     using type = uint16_t;
 };
 
+// Bytes [sh, sh + 16) of the 32-byte string lo:hi, sh below 16 and a multiple
+// of T's size: two rounds of selections by sh's bits, and for 16-bit elements
+// a shift.
+template <typename T>
+__device__ __forceinline__ uint4 shifted(uint4 lo, uint4 hi, unsigned sh) {
+    const bool two = sh & 8u, one = sh & 4u;
+    const uint32_t a0 = two ? lo.z : lo.x, a1 = two ? lo.w : lo.y, a2 = two ? hi.x : lo.z, a3 = two ? hi.y : lo.w;
+    const uint32_t a4 = two ? hi.z : hi.x, a5 = two ? hi.w : hi.y;
+    uint4 v = make_uint4(one ? a1 : a0, one ? a2 : a1, one ? a3 : a2, one ? a4 : a3);
+    if (sizeof(T) == 2) {
+        const uint32_t last = one ? a5 : a4;
+        const unsigned r = (sh & 2u) * 8u;
+        v = make_uint4(__funnelshift_r(v.x, v.y, r), __funnelshift_r(v.y, v.z, r), __funnelshift_r(v.z, v.w, r),
+                       __funnelshift_r(v.w, last, r));
+    }
+    return v;
+}
+
 // The n (1..8) columns from c on of a row, at any alignment; the others are
 // zero. A shifted granule is put together from the 16-byte blocks that hold
 // it, each of which has at least one byte of the row.
 template <typename T>
 __device__ __forceinline__ void load_granule(Raw<T>& r, const T* row, int64_t c, int n) {
+    constexpr int kV = Raw<T>::kVec;
     if (n == kGran) {
-        load_raw_at<T>(r, reinterpret_cast<uintptr_t>(row + c));
+        const uintptr_t at = reinterpret_cast<uintptr_t>(row + c);
+        const unsigned sh = (unsigned)(at & 15u);
+        const uint4* q = reinterpret_cast<const uint4*>(at - sh);
+        if (sh == 0) {
+#pragma unroll
+            for (int v = 0; v < kV; ++v) put(r.w + 4 * v, ld_stream(q + v));
+        } else {
+            uint4 b[kV + 1];
+#pragma unroll
+            for (int v = 0; v <= kV; ++v) b[v] = ld_reuse(q + v);
+#pragma unroll
+            for (int v = 0; v < kV; ++v) put(r.w + 4 * v, shifted<T>(b[v], b[v + 1], sh));
+        }
         return;
     }
     zero_raw(r);
@@ -77,7 +108,6 @@ __device__ __forceinline__ void store_span(T* p, const Raw<T>& r, int n, int lan
     below.y = __shfl_up_sync(kFull, l[1], 1);
     below.z = __shfl_up_sync(kFull, l[2], 1);
     below.w = __shfl_up_sync(kFull, l[3], 1);
-    const int nextn = __shfl_down_sync(kFull, n, 1);
     const int head = (int)sh / (int)sizeof(T);  // elements of the first block below p
     if (n == kGran && lane > 0) {
         uint4* q = reinterpret_cast<uint4*>(reinterpret_cast<uintptr_t>(p) - sh);
@@ -85,12 +115,32 @@ __device__ __forceinline__ void store_span(T* p, const Raw<T>& r, int n, int lan
         for (int v = 0; v < kV; ++v) {
             const uint4 lo = v == 0 ? below : make_uint4(r.w[4 * v - 4], r.w[4 * v - 3], r.w[4 * v - 2], r.w[4 * v - 1]);
             const uint4 hi = make_uint4(r.w[4 * v], r.w[4 * v + 1], r.w[4 * v + 2], r.w[4 * v + 3]);
-            st_stream(q + v, funnel(lo, hi, 16u - sh));
+            st_stream(q + v, shifted<T>(lo, hi, 16u - sh));
         }
     }
-    // what no whole block of this or the next lane covers: the span's first
-    // kGran - head elements, a short granule, and the last head elements of a
-    // granule whose upper neighbour stores no whole block
+    if (__all_sync(kFull, n == kGran)) {
+        // the first lane's elements before the second's block, and the last
+        // lane's behind its own: eight in all, one for each of the first lanes
+        const int e = lane & 7, from = e < kGran - head ? 0 : 31;
+        uint32_t v = 0;
+#pragma unroll
+        for (int i = 0; i < Raw<T>::kWords; ++i) {
+            const uint32_t x = __shfl_sync(kFull, r.w[i], from);
+            v = i == e * (int)sizeof(T) / 4 ? x : v;
+        }
+        if (lane < 8) {
+            T* q = p - lane * kGran + (from ? 31 * kGran : 0) + e;
+            if constexpr (sizeof(T) == 4)
+                *reinterpret_cast<uint32_t*>(q) = v;
+            else
+                *q = (T)(v >> ((e & 1) * 16));
+        }
+        return;
+    }
+    // a row's last span. What no whole block of this or the next lane covers:
+    // the first lane's first kGran - head elements, a short granule, and the
+    // last head elements of a granule whose upper neighbour stores no block
+    const int nextn = __shfl_down_sync(kFull, n, 1);
     const bool whole = n == kGran && lane > 0;
     const bool covered = lane < 31 && nextn == kGran;
     const int first = whole ? kGran - head : 0;
@@ -189,6 +239,7 @@ __device__ __forceinline__ void round_to(const Cols& x, Raw<float>& r) {
 }
 // Columns past a row's end become 0.
 __device__ __forceinline__ void cut(Cols& x, int n) {
+    if (n == kGran) return;
 #pragma unroll
     for (int e = 0; e < 8; ++e)
         if (e >= n) x.set(e, 0.0f);
@@ -221,7 +272,7 @@ __device__ __forceinline__ void span_fetch(uint4* slot, const T* row, int c0, in
     constexpr int kV = Raw<T>::kVec;
     const uintptr_t from = reinterpret_cast<uintptr_t>(row + c0);
     const int sh = kAligned ? 0 : (int)(from & 15u);
-    const int bytes = cols > c0 ? (cols - c0) * (int)sizeof(T) + sh : 0;
+    const int bytes = cols > c0 ? (cols - c0) * (int)sizeof(T) + sh : 0;  // all of the row's: blocks past the span are not asked for
 #pragma unroll
     for (int v = 0; v < kV + (kAligned ? 0 : 1); ++v) {
         const int b = v * 32 + lane;
@@ -245,7 +296,7 @@ __device__ __forceinline__ void span_read(Raw<T>& r, const uint4* slot, const T*
     }
     b[kV] = slot[lane * kV + kV];
 #pragma unroll
-    for (int v = 0; v < kV; ++v) put(r.w + 4 * v, funnel(b[v], b[v + 1], sh));
+    for (int v = 0; v < kV; ++v) put(r.w + 4 * v, shifted<T>(b[v], b[v + 1], sh));
 }
 
 // ------------------------------------------------------------- dropout mask
@@ -306,10 +357,11 @@ __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontr
 __device__ __forceinline__ void allow_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 template <typename... A>
-cudaError_t launch_next(void (*kernel)(A...), dim3 grid, int block, cudaStream_t s, A... args) {
+cudaError_t launch_next(void (*kernel)(A...), dim3 grid, int block, int smem, cudaStream_t s, A... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)block);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
