@@ -5,11 +5,11 @@
 //
 // Gradient: grad_table[v] = scale * sum of grad_out[t] over the tokens t of
 // row v. Three kernels, each launched while the one before it runs:
-//   1. a stable radix sort of (row, token) by one cluster of blocks, which
-//      also marks the rows that a token names;
+//   1. a stable radix sort of (row, token) by one cluster of blocks;
 //   2. sums: a warp adds up the gradients of a chunk of sorted tokens for a
 //      span of 256 columns, writes the rows that lie inside the chunk, leaves
-//      partial sums of those that cross its ends, and lists these;
+//      partial sums of those that cross its ends, and lists these; it also
+//      marks the rows that a token names;
 //   3. the partial sums of the listed rows, added in order, and beside them
 //      the zeros of the rows that are not marked.
 #include "fsdp_ops.cuh"
@@ -349,49 +349,43 @@ __global__ void __launch_bounds__(kSortThreads)
             if (r < blocks) count += (int)cluster_read(&sm.total[1 << bits], r);
         *w.count = count;
     }
-    if (!a.accumulate) {
-        // a row's first token marks it
-        const int2* sorted = w.sorted[(passes - 1) & 1];
-#pragma unroll 4
-        for (int64_t i = rank * kSortThreads + tid; i < a.n; i += blocks * kSortThreads) {
-            const int row = __ldcg(&sorted[i].x), prev = i > 0 ? __ldcg(&sorted[i - 1].x) : -1;
-            if (row != prev && row < a.vocab) atomicOr(w.marks + (row >> 5), 1u << (row & 31));
-        }
-    }
     cluster_sync();  // no block leaves while another reads its counts
 }
 
 // The same for up to kFewTokens tokens, one block: a token's place is the
 // number of tokens that come before it.
-__global__ void __launch_bounds__(kFewTokens) embedding_few_kernel(EmbeddingGradArgs a, GradWork w) {
+__global__ void __launch_bounds__(2 * kFewTokens) embedding_few_kernel(EmbeddingGradArgs a, GradWork w) {
     __shared__ int4 keys[kFewTokens / 4];
-    __shared__ int named;
+    __shared__ int place[kFewTokens], named;
     allow_next();
-    const int tid = threadIdx.x, n = (int)a.n;
+    // two threads a token, each for half of the others
+    const int tid = threadIdx.x % kFewTokens, half = threadIdx.x / kFewTokens, n = (int)a.n, quads = (n + 3) / 4;
     const int row = tid < n ? row_of(read_id(a.ids, a.wide_ids, tid), a.first, a.vocab) : 0x7fffffff;
-    reinterpret_cast<int*>(keys)[tid] = row;
-    if (tid == 0) {
+    if (half == 0) {
+        reinterpret_cast<int*>(keys)[tid] = row;
+        place[tid] = 0;
+    }
+    if (threadIdx.x == 0) {
         named = 0;
         *w.crossings = 0;
     }
     if (!a.accumulate)
-        for (int64_t i = tid; i < (a.vocab + 31) / 32; i += kFewTokens) w.marks[i] = 0;
+        for (int64_t i = threadIdx.x; i < (a.vocab + 31) / 32; i += 2 * kFewTokens) w.marks[i] = 0;
     __syncthreads();
-    int at = 0;
     if (tid < n) {
-        for (int j = 0; j < (n + 3) / 4; ++j) {
+        int before = 0;
+#pragma unroll 4
+        for (int j = half * (quads / 2); j < (half ? quads : quads / 2); ++j) {
             const int4 k = keys[j];
-            at += (k.x < row || (k.x == row && 4 * j < tid)) + (k.y < row || (k.y == row && 4 * j + 1 < tid)) +
-                  (k.z < row || (k.z == row && 4 * j + 2 < tid)) + (k.w < row || (k.w == row && 4 * j + 3 < tid));
+            before += (k.x < row || (k.x == row && 4 * j < tid)) + (k.y < row || (k.y == row && 4 * j + 1 < tid)) +
+                      (k.z < row || (k.z == row && 4 * j + 2 < tid)) + (k.w < row || (k.w == row && 4 * j + 3 < tid));
         }
-        w.sorted[0][at] = make_int2(row, tid);
-        if (row < a.vocab) {
-            atomicAdd(&named, 1);
-            if (!a.accumulate) atomicOr(w.marks + (row >> 5), 1u << (row & 31));
-        }
+        atomicAdd(&place[tid], before);
+        if (half == 0 && row < a.vocab) atomicAdd(&named, 1);
     }
     __syncthreads();
-    if (tid == 0) *w.count = named;
+    if (half == 0 && tid < n) w.sorted[0][place[tid]] = make_int2(row, tid);
+    if (threadIdx.x == 0) *w.count = named;
 }
 
 // ------------------------------------------------------------ gradient: zeros and sums
@@ -483,8 +477,8 @@ __global__ void __launch_bounds__(32 * kEmbWarps, sizeof(S) == 4 ? 3 : 5)
     const int g = (int)(it - chunk * spans) * 32 + lane, n = granule_cols((int64_t)g, a.cols);
     const int64_t c = (int64_t)g * kGran, c0 = c - lane * kGran;
     const int left = (int)(a.cols - c0 < kSpan ? a.cols - c0 : kSpan);
+    allow_next();
     wait_for_previous();
-    allow_next();  // not before: the next kernel's zeros need the sort's marks
     const int count = min(__ldcg(w.count), (int)a.n);
     if (chunk * w.chunk >= count) return;
     const int lo = (int)chunk * w.chunk, m = count - lo < w.chunk ? count - lo : w.chunk;
@@ -494,6 +488,10 @@ __global__ void __launch_bounds__(32 * kEmbWarps, sizeof(S) == 4 ? 3 : 5)
     mine = make_int2(min(mine.x, (int)a.vocab - 1), (int)min((unsigned)mine.y, (unsigned)a.n - 1));
     const int prev = lo > 0 ? __ldcg(&sorted[lo - 1].x) : -1;
     const int next = lo + m < count ? __ldcg(&sorted[lo + m].x) : -1;
+    if (!a.accumulate && g < 32) {  // once, with the first span: a row's first token marks it
+        const int before = __shfl_up_sync(kFull, mine.x, 1);
+        if (lane < m && mine.x != (lane ? before : prev)) atomicOr(w.marks + (mine.x >> 5), 1u << (mine.x & 31));
+    }
     auto gradient = [&](int j) {
         return static_cast<const S*>(a.grad.data) + (int64_t)__shfl_sync(kFull, mine.y, j & 31) * a.grad.stride + c0;
     };
@@ -555,22 +553,19 @@ __device__ __forceinline__ bool sound(const EmbeddingGradArgs& a, const GradWork
 // The first spans * y blocks, block (span, y): the rows that cross chunks, for
 // a span of columns. Its warps take the listed rows of up to kShort parts in
 // turn, one each, and then the others together, a share of the parts each. The
-// other blocks write zeros and need not wait for the sums (no block of which
-// allowed this kernel before the sort, whose marks they read, had ended); the
-// last one does so in the end, that this kernel may not end before the sums.
+// other blocks write zeros.
 constexpr int kShort = 8;
 template <typename D, bool kAligned>
 __global__ void __launch_bounds__(32 * kEmbWarps) embedding_join_kernel(EmbeddingGradArgs a, GradWork w, int spans, int ys, int per) {
     __shared__ float4 sums[kEmbWarps][2][32];
+    wait_for_previous();
     if ((int)blockIdx.x >= spans * ys) {
         write_zeros<D>(a, w.nchunks ? w.marks : nullptr, blockIdx.x - spans * ys, per);
-        if (blockIdx.x + 1 == gridDim.x) wait_for_previous();
         return;
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, y = blockIdx.x / spans;
     const int64_t g = (int64_t)(blockIdx.x - y * spans) * 32 + lane, c = g * kGran;
     const int n = granule_cols(g, a.cols);
-    wait_for_previous();
     const int crossings = min(__ldcg(w.crossings), w.nchunks);
     for (int i = y * kEmbWarps + warp; i < crossings; i += ys * kEmbWarps) {
         const int4 x = __ldcg(reinterpret_cast<const int4*>(w.cross + i));
@@ -613,7 +608,7 @@ cudaError_t embedding_grad_as(const EmbeddingGradArgs& a, cudaStream_t s) {
     if (sums > 0x7fffffff || zeros + (int64_t)spans * ys > 0x7fffffff) return cudaErrorInvalidValue;
     cudaError_t e = cudaSuccess;
     if (few && a.n > 0) {
-        embedding_few_kernel<<<1, kFewTokens, 0, s>>>(a, w);
+        embedding_few_kernel<<<1, 2 * kFewTokens, 0, s>>>(a, w);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         count_launch();
     } else if (a.n > 0) {
@@ -649,7 +644,7 @@ cudaError_t embedding_grad_as(const EmbeddingGradArgs& a, cudaStream_t s) {
     if (grid.x == 0) return cudaSuccess;
     if (a.n > 0) {
         e = launch_next(embedding_join_kernel<D, kAligned>, grid, 32 * kEmbWarps, 0, s, a, w, spans, ys, per);
-    } else {  // nothing before it, and so nothing for its zeros to run beside
+    } else {  // nothing of this call before it
         embedding_join_kernel<D, kAligned><<<grid, 32 * kEmbWarps, 0, s>>>(a, w, spans, ys, per);
         e = cudaGetLastError();
     }
