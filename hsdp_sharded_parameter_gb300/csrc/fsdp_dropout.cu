@@ -67,8 +67,41 @@ __global__ void __launch_bounds__(32 * kDropWarps, 4) dropout_kernel(DropoutArgs
     }
 }
 
+// Narrow rows of grans granules, items granules in all.
+template <typename T, bool kAligned>
+__global__ void __launch_bounds__(32 * kDropWarps) dropout_narrow_kernel(DropoutArgs a, uint32_t grans, uint32_t items) {
+    const uint32_t i0 = blockIdx.x * (kNarrow * blockDim.x) + threadIdx.x;
+    Raw<T> in[kNarrow], add[kNarrow];
+#pragma unroll
+    for (int u = 0; u < kNarrow; ++u) {
+        const uint32_t i = i0 + u * blockDim.x, row = i / grans, g = i - row * grans;
+        const int n = i < items ? granule_cols((int64_t)g, a.cols) : 0;
+        load_cols<kAligned>(in[u], static_cast<const T*>(a.x.data) + row * a.x.stride, g * kGran, n);
+        if (a.res.data) load_cols<kAligned>(add[u], static_cast<const T*>(a.res.data) + row * a.res.stride, g * kGran, n);
+    }
+#pragma unroll
+    for (int u = 0; u < kNarrow; ++u) {
+        const uint32_t i = i0 + u * blockDim.x, row = i / grans, g = i - row * grans;
+        if (i >= items) break;
+        const Cols v = widened(in[u]);
+        Cols y = a.res.data ? widened(add[u]) : all(0.0f);
+        if (a.mask.drops)
+            add_dropped(y, v, a.mask, row, g);
+        else
+            y = y + v;
+        round_to(y, in[u]);
+        store_granule(static_cast<T*>(a.out.data) + row * a.out.stride + g * kGran, in[u], granule_cols((int64_t)g, a.cols));
+    }
+}
+
 template <typename T, bool kAligned>
 void dropout(const DropoutArgs& a, cudaStream_t s) {
+    if (narrow_rows(a.rows, a.cols, kAligned)) {
+        const uint32_t grans = (uint32_t)((a.cols + kGran - 1) / kGran), items = (uint32_t)a.rows * grans;
+        const uint32_t each = kNarrow * 32 * kDropWarps;
+        dropout_narrow_kernel<T, kAligned><<<(items + each - 1) / each, 32 * kDropWarps, 0, s>>>(a, grans, items);
+        return;
+    }
     const int64_t span = kSpan * kDropSpans<T>, steps = (a.cols + span - 1) / span, items = steps * a.rows;
     const int64_t blocks = (items + kDropWarps - 1) / kDropWarps;
     const unsigned grid = (unsigned)(blocks < 0x7fffffff ? blocks : 0x7fffffff);

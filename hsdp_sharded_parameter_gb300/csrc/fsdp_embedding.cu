@@ -75,6 +75,30 @@ __global__ void __launch_bounds__(32 * kEmbWarps) embedding_kernel(EmbeddingArgs
     }
 }
 
+// Narrow rows of grans granules, items granules in all.
+template <typename S, typename D, bool kAligned>
+__global__ void __launch_bounds__(32 * kEmbWarps) embedding_narrow_kernel(EmbeddingArgs a, uint32_t grans, uint32_t items) {
+    const uint32_t i0 = blockIdx.x * (kNarrow * blockDim.x) + threadIdx.x;
+    Raw<S> in[kNarrow];
+    bool named[kNarrow];
+#pragma unroll
+    for (int u = 0; u < kNarrow; ++u) {
+        const uint32_t i = i0 + u * blockDim.x, t = i / grans, g = i - t * grans;
+        const int64_t row = i < items ? row_of(read_id(a.ids, a.wide_ids, t), a.first, a.vocab) : a.vocab;
+        named[u] = row < a.vocab;
+        if (named[u])
+            load_cols<kAligned>(in[u], static_cast<const S*>(a.table.data) + row * a.table.stride, g * kGran, granule_cols((int64_t)g, a.cols));
+    }
+#pragma unroll
+    for (int u = 0; u < kNarrow; ++u) {
+        const uint32_t i = i0 + u * blockDim.x, t = i / grans, g = i - t * grans;
+        if (i >= items) break;
+        Raw<D> r;
+        round_to(named[u] ? widened(in[u]) * all(a.scale) : all(0.0f), r);
+        store_granule(static_cast<D*>(a.out.data) + t * a.out.stride + g * kGran, r, granule_cols((int64_t)g, a.cols));
+    }
+}
+
 // ------------------------------------------------- gradient: the sort
 
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
@@ -665,7 +689,14 @@ cudaError_t embedding(const EmbeddingArgs& a, cudaStream_t s) {
     const int64_t blocks = (items + kEmbWarps - 1) / kEmbWarps;
     const unsigned grid = (unsigned)(blocks < 0x7fffffff ? blocks : 0x7fffffff);
     const bool aligned = a.cols % kGran == 0 && on_grid(a.table, sizeof(S)) && on_grid(a.out, sizeof(D));
-    if (aligned)
+    if (narrow_rows(a.n, a.cols, aligned)) {
+        const uint32_t grans = (uint32_t)((a.cols + kGran - 1) / kGran), all = (uint32_t)a.n * grans;
+        const uint32_t each = kNarrow * 32 * kEmbWarps, blocks32 = (all + each - 1) / each;
+        if (aligned)
+            embedding_narrow_kernel<S, D, true><<<blocks32, 32 * kEmbWarps, 0, s>>>(a, grans, all);
+        else
+            embedding_narrow_kernel<S, D, false><<<blocks32, 32 * kEmbWarps, 0, s>>>(a, grans, all);
+    } else if (aligned)
         embedding_kernel<S, D, true><<<grid, 32 * kEmbWarps, 0, s>>>(a, steps, per, items);
     else
         embedding_kernel<S, D, false><<<grid, 32 * kEmbWarps, 0, s>>>(a, steps, per, items);

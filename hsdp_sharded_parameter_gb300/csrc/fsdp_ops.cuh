@@ -150,6 +150,29 @@ __device__ __forceinline__ void store_span(T* p, const Raw<T>& r, int n, int lan
         if (e >= first && e < last) store_elem(p + e, r, e);
 }
 
+// A granule stored by one thread, at any alignment.
+template <typename T>
+__device__ __forceinline__ void store_granule(T* p, const Raw<T>& r, int n) {
+    if (n == kGran && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+        store_raw(p, r);
+    } else {
+#pragma unroll
+        for (int e = 0; e < kGran; ++e)
+            if (e < n) store_elem(p + e, r, e);
+    }
+}
+
+// Narrow rows: kernels that give a warp a span of a row would leave most of
+// its lanes or of its loads unused, so a thread takes granules of any rows,
+// kNarrow of them. On one GB300, dropout of 32768 rows of bf16 with a residual,
+// by threads and by spans: 20 columns 5.9 and 40 us, 200 8 and 25, 1000 33 and
+// 30. Off the 16-byte grid a thread stores element by element, and spans are
+// ahead sooner (lookup of 32768 tokens, 201 columns: 20 and 12 us).
+constexpr int kNarrow = 4, kNarrowCols = 512, kNarrowShifted = 96;
+inline bool narrow_rows(int64_t rows, int64_t cols, bool aligned) {
+    return cols <= (aligned ? kNarrowCols : kNarrowShifted) && rows * ((cols + kGran - 1) / kGran) < ((int64_t)1 << 31);
+}
+
 // The granules of a warp's span, as load_granule and store_span do them, where
 // kAligned says that every row starts on the 16-byte grid and holds whole
 // granules (n is 8, or 0 past the row's end).
