@@ -17,18 +17,6 @@
 // depend on how many warps fit beside the row's registers.
 #include "fsdp_ops.cuh"
 
-#ifndef TW
-#define TW 3
-#endif
-#ifndef TV
-#define TV 1
-#endif
-#ifndef TX
-#define TX 32
-#endif
-#ifndef TS
-#define TS 200
-#endif
 namespace fsdp {
 namespace {
 
@@ -307,7 +295,7 @@ __device__ __forceinline__ float2 pair_end(float v, int gw, int lane, const floa
 // with the gradient right behind its sums, the 16 warps that the columns'
 // sums leave room for waited for each other (8192 columns: 327 us, now 250).
 template <typename T, int V, bool kAligned, int kMode>
-__global__ void __launch_bounds__(V == 1 ? 256 : 512, V == 1 ? TW : 1)
+__global__ void __launch_bounds__(32 * kWarps, V == 1 ? 2 : 1)
     norm_grad_kernel(NormGradArgs a, int gw, int depth, int64_t stride) {
     extern __shared__ uint4 ring[];
     __shared__ float part[2][kWarps * 32];
@@ -391,13 +379,14 @@ __global__ void __launch_bounds__(V == 1 ? 256 : 512, V == 1 ? TW : 1)
     __syncwarp();
     float sum = sums(row, 0, mean, rstd, &part[0][w * 32]);
     int slot = 0, side = 0;
-    // every group of a block goes round as often, for the barriers
-    for (uint32_t r0 = blockIdx.x * groups; r0 < rows; r0 += step, row += step) {
+    for (; row < rows; row += step) {
         __syncwarp();  // the last reads of the slot that is filled now
         fetch(row + (depth - 1) * step, slot == 0 ? depth - 1 : slot - 1);
         async_wait_but(depth - 2);
-        if (gw > 1)
+        if (groups == 1)
             __syncthreads();
+        else if (gw > 1)  // the group's own barrier
+            asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(gw * 32) : "memory");
         else
             __syncwarp();
         const float2 c = pair_end(sum, gw, lane, &part[side][group * gw * 32]);
@@ -408,27 +397,25 @@ __global__ void __launch_bounds__(V == 1 ? 256 : 512, V == 1 ? TW : 1)
             r = __ldg(a.rstd + row + 2 * step);
         }
         sum = sums(row + step, after, next_mean, next_rstd, &part[side ^ 1][w * 32]);
-        if (row < rows) {
-            const Cols k0 = all(rstd), k1 = all(-(c.x * inv)), k2 = all(-(c.y * inv));
+        const Cols k0 = all(rstd), k1 = all(-(c.x * inv)), k2 = all(-(c.y * inv));
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int g = (v * gw + warp) * 32 + lane, c0 = (v * gw + warp) * kSpan, n = granule_cols(g, cols);
-                Cols dy, u;
-                read(v, slot, row, mean, rstd, n, dy, u);
-                if (!kAligned || n) {
-                    db[v] = db[v] + dy;
-                    dw[v] = fma(dy, u, dw[v]);
-                }
-                Cols t = fma(u, k2, fma(dy, weight(v, g, n), k1));
-                if (has<kMode>(kResidual, a.grad_hidden.data)) {
-                    Raw<T> q;
-                    span_read<kAligned>(q, mine + (slot * streams * V + 2 * V + v) * kOne, row_at<const T>(a.grad_hidden.data, row, as), c0, lane);
-                    t = fma(t, k0, widened(q));
-                } else {
-                    t = t * k0;
-                }
-                store_grad<kAligned, kMode>(a, t, row, g, n, lane, row_at<T>(a.grad_res.data, row, rs), row_at<T>(a.grad_x.data, row, xs));
+        for (int v = 0; v < V; ++v) {
+            const int g = (v * gw + warp) * 32 + lane, c0 = (v * gw + warp) * kSpan, n = granule_cols(g, cols);
+            Cols dy, u;
+            read(v, slot, row, mean, rstd, n, dy, u);
+            if (!kAligned || n) {
+                db[v] = db[v] + dy;
+                dw[v] = fma(dy, u, dw[v]);
             }
+            Cols t = fma(u, k2, fma(dy, weight(v, g, n), k1));
+            if (has<kMode>(kResidual, a.grad_hidden.data)) {
+                Raw<T> q;
+                span_read<kAligned>(q, mine + (slot * streams * V + 2 * V + v) * kOne, row_at<const T>(a.grad_hidden.data, row, as), c0, lane);
+                t = fma(t, k0, widened(q));
+            } else {
+                t = t * k0;
+            }
+            store_grad<kAligned, kMode>(a, t, row, g, n, lane, row_at<T>(a.grad_res.data, row, rs), row_at<T>(a.grad_x.data, row, xs));
         }
         mean = next_mean;
         rstd = next_rstd;
@@ -543,12 +530,11 @@ __global__ void __launch_bounds__(256) norm_param_kernel(NormGradArgs a, int64_t
 
 // Adds the parts' sums, 32 columns a block, a share of the parts for each of
 // its warps: blockIdx.y 0 the weight's, 1 the bias's.
-constexpr int kJoinWarps = 16;
 template <typename G>
-__global__ void __launch_bounds__(32 * kJoinWarps)
+__global__ void __launch_bounds__(1024)
     norm_join_kernel(const float* work, int64_t stride, int parts, int64_t cols, int accumulate, G* gw, G* gb) {
-    __shared__ float sums[kJoinWarps][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __shared__ float sums[32][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;
     G* out = blockIdx.y ? gb : gw;
     wait_for_previous();
@@ -557,14 +543,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     if (c < cols) {
         const float* from = work + blockIdx.y * stride + c;
 #pragma unroll 8
-        for (int p = parts * warp / kJoinWarps; p < parts * (warp + 1) / kJoinWarps; ++p) s += __ldcg(from + 2 * (int64_t)p * stride);
+        for (int p = parts * warp / warps; p < parts * (warp + 1) / warps; ++p) s += __ldcg(from + 2 * (int64_t)p * stride);
     }
     sums[warp][lane] = s;
     __syncthreads();
     if (warp != 0 || c >= cols) return;
     s = 0.0f;
-#pragma unroll
-    for (int q = 0; q < kJoinWarps; ++q) s += sums[q][lane];
+    for (int q = 0; q < warps; ++q) s += sums[q][lane];
     if (accumulate) s += load_f32(out, c);
     store_f32(out, c, s);
 }
@@ -577,7 +562,7 @@ bool fits_32(const Mat& m, int es) { return m.stride < ((int64_t)1 << 32) / es; 
 
 // What the blocks of an SM may take of shared memory together: the rest of
 // its 256 KB is the L1 cache, where the parameters stay.
-constexpr int64_t kSmemPerSm = 132 * 1024, kSmemMost = TS * 1024;
+constexpr int64_t kSmemPerSm = 132 * 1024, kSmemMost = 200 * 1024;
 
 // How a kernel is launched on rows of these columns: V granules a thread, gw
 // warps a row, groups of them in a block, blocks of an SM, and the rows that
@@ -648,13 +633,17 @@ cudaError_t norm(const NormArgs& a, cudaStream_t s) {
 
 Shape grad_shape(int64_t rows, int64_t cols, int streams, int slot_bytes) {
     Shape f;
-    const int64_t grans = (cols + kGran - 1) / kGran;
-    f.v = grans <= 32 * TV ? 1 : (grans <= 32 * TX ? 2 : 4);
-    f.gw = (int)((grans + 32 * f.v - 1) / (32 * f.v));
-    f.groups = f.gw >= 4 ? 1 : 4 / f.gw;
-    const int block = 32 * f.gw * f.groups;
-    f.per_sm = (f.v == 1 ? 256 * TW : 512) / block;
-    if (f.per_sm < 1) f.per_sm = 1;
+    // 2 granules a thread where they will do: with 3 or 4 the weight has to be
+    // loaded again for every row (16384 rows of 6144 bf16: 135 us with 2, 12
+    // warps and the fourth quarter of the SM's idle, 193 with 3 and all 16)
+    const int spans = (int)((cols + kSpan - 1) / kSpan);
+    f.v = spans <= 1 ? 1 : (spans <= 2 * kWarps ? 2 : (spans <= 3 * kWarps ? 3 : 4));
+    f.gw = (spans + f.v - 1) / f.v;
+    // a block takes as many rows at a time as it has warps for, and as there
+    // are rows for all SMs: the fewer blocks, the fewer sums to add in the end
+    const int64_t most_groups = kWarps / f.gw, share = (rows + sm_count() - 1) / sm_count();
+    f.groups = (int)(share < most_groups ? share : most_groups);
+    f.per_sm = f.v == 1 ? 2 : 1;
     const int64_t need = (rows + f.groups - 1) / f.groups;
     const int64_t most = (int64_t)sm_count() * f.per_sm;
     f.grid = (int)(need < most ? need : most);
@@ -682,7 +671,8 @@ cudaError_t grad_rows(const NormGradArgs& a, const Shape& f, int64_t stride, cud
 template <typename T, bool kAligned, int kMode>
 cudaError_t grad_v(const NormGradArgs& a, const Shape& f, int64_t stride, cudaStream_t s) {
     return f.v == 1 ? grad_rows<T, 1, kAligned, kMode>(a, f, stride, s)
-           : f.v == 2 ? grad_rows<T, 2, kAligned, kMode>(a, f, stride, s) : grad_rows<T, 4, kAligned, kMode>(a, f, stride, s);
+           : f.v == 2 ? grad_rows<T, 2, kAligned, kMode>(a, f, stride, s)
+           : f.v == 3 ? grad_rows<T, 3, kAligned, kMode>(a, f, stride, s) : grad_rows<T, 4, kAligned, kMode>(a, f, stride, s);
 }
 
 constexpr int kWideParts = 256;
@@ -745,13 +735,14 @@ cudaError_t launch_norm_grad(int dt, int param_grad_dt, const NormGradArgs& a, c
     }
     if (!a.grad_weight && !a.grad_bias) return cudaSuccess;
     const dim3 grid((unsigned)((a.cols + 31) / 32), 2);
+    const int block = grid.x < (unsigned)sm_count() ? 1024 : 512;  // many warps a block where there are few blocks
     const float* work = a.work;
     const int64_t stride = grad_stride(a.cols);
     count_launch();
     if (param_grad_dt == FSDP_F32)
-        return launch_next(norm_join_kernel<float>, grid, 32 * kJoinWarps, 0, s, work, stride, parts, a.cols, a.accumulate,
+        return launch_next(norm_join_kernel<float>, grid, block, 0, s, work, stride, parts, a.cols, a.accumulate,
                            static_cast<float*>(a.grad_weight), static_cast<float*>(a.grad_bias));
-    return launch_next(norm_join_kernel<uint16_t>, grid, 32 * kJoinWarps, 0, s, work, stride, parts, a.cols, a.accumulate,
+    return launch_next(norm_join_kernel<uint16_t>, grid, block, 0, s, work, stride, parts, a.cols, a.accumulate,
                        static_cast<uint16_t*>(a.grad_weight), static_cast<uint16_t*>(a.grad_bias));
 }
 
