@@ -575,10 +575,14 @@ struct Shape {
 Shape norm_shape(int64_t rows, int64_t cols, int streams, int slot_bytes) {
     Shape f;
     const int64_t grans = (cols + kGran - 1) / kGran;
-    // few warps a row make its two sums cheap; 4 granules a thread and two
-    // blocks of 8 warps ran 8192 columns in 182 us, 2 granules and 16 warps
-    // in 202 (16384 rows of bf16, dropout and residual)
-    f.v = grans <= 32 * 4 ? 1 : (grans <= 32 * 16 ? 2 : 4);
+    // few warps a row make its two sums cheap: 16384 rows of bf16 with dropout
+    // and residual take 29 us at 1024 columns with 2 granules a thread and 33
+    // with 1, 95 at 4096 with 4 and 113 with 2, 182 at 8192 with 4 and 202
+    // with 2. Rows that do not fill the GPU are done sooner by more warps (16
+    // of 4096 columns: 3.6 us with 2 granules, 4.2 with 4).
+    const int spans = (int)((cols + kSpan - 1) / kSpan);
+    const bool few = rows <= 2 * (int64_t)sm_count();
+    f.v = spans <= (few ? 4 : 1) ? 1 : (spans <= (few ? 16 : 8) ? 2 : 4);
     f.gw = (int)((grans + 32 * f.v - 1) / (32 * f.v));
     f.groups = f.gw >= 4 ? 1 : 4 / f.gw;
     const int block = 32 * f.gw * f.groups;
