@@ -4,7 +4,7 @@
 // no row.
 //
 // Gradient: grad_table[v] = scale * sum of grad_out[t] over the tokens t of
-// row v. Three kernels, each launched while the one before it runs:
+// row v. One kernel for few tokens (below); else three, each launched while the one before it runs:
 //   1. a stable radix sort of (row, token) by one cluster of blocks;
 //   2. sums: a warp adds up the gradients of a chunk of sorted tokens for a
 //      span of 256 columns, writes the rows that lie inside the chunk, leaves
@@ -31,13 +31,26 @@ __device__ __forceinline__ int row_of(int64_t id, int64_t first, int64_t vocab) 
 
 // ------------------------------------------------------------------ forward
 
-// A warp takes up to kEmbSpans neighbouring spans of 256 columns of a token.
-constexpr int kEmbSpans = 4;
+// The table's columns of a granule of an aligned row. Rows are looked up again,
+// so they are not marked for early eviction as streams are.
+template <typename T>
+__device__ __forceinline__ void load_table(Raw<T>& r, const T* row, int64_t c, int n) {
+    if (n == 0) return;
+    const uint4* q = reinterpret_cast<const uint4*>(row + c);
+#pragma unroll
+    for (int v = 0; v < Raw<T>::kVec; ++v) put(r.w + 4 * v, ld_reuse(q + v));
+}
+
+// A warp takes up to kEmbSpans neighbouring spans of 256 columns of a token:
+// 32768 tokens of 8192 bf16 take 116 us with 8, 121 with 4 and 141 with 2; to
+// fp32 268, 250 and 225.
+template <typename S, typename D>
+constexpr int kEmbSpans = sizeof(D) == 4 ? 2 : (sizeof(S) == 4 ? 4 : 8);
 
 template <typename S, typename D, bool kAligned>
 __global__ void __launch_bounds__(32 * kEmbWarps) embedding_kernel(EmbeddingArgs a, int64_t steps, int per, int64_t items) {
     // rows off the 16-byte grid come in through shared memory
-    __shared__ uint4 staged[kAligned ? 1 : kEmbWarps][kAligned ? 1 : kEmbSpans][kAligned ? 1 : kSlot<false, S>];
+    __shared__ uint4 staged[kAligned ? 1 : kEmbWarps][kAligned ? 1 : kEmbSpans<S, D>][kAligned ? 1 : kSlot<false, S>];
     const int lane = threadIdx.x & 31;
     uint4(*const mine)[kAligned ? 1 : kSlot<false, S>] = staged[kAligned ? 0 : threadIdx.x >> 5];
     for (int64_t it = warp_id(); it < items; it += warp_count()) {
@@ -47,12 +60,12 @@ __global__ void __launch_bounds__(32 * kEmbWarps) embedding_kernel(EmbeddingArgs
         const S* from = static_cast<const S*>(a.table.data) + row * a.table.stride;
         D* to = static_cast<D*>(a.out.data) + t * a.out.stride;
         const int left = (int)(a.cols - c0 < per * kSpan ? a.cols - c0 : per * kSpan);
-        Raw<S> in[kEmbSpans];
+        Raw<S> in[kEmbSpans<S, D>];
 #pragma unroll
-        for (int u = 0; u < kEmbSpans; ++u) {
+        for (int u = 0; u < kEmbSpans<S, D>; ++u) {
             if (!named || u >= per) break;
             if constexpr (kAligned)
-                load_cols<true>(in[u], from, (g0 + u * 32) * kGran, granule_cols(g0 + u * 32, a.cols));
+                load_table(in[u], from, (g0 + u * 32) * kGran, granule_cols(g0 + u * 32, a.cols));
             else
                 span_fetch<false>(mine[u], from + c0, u * kSpan, left, lane);
         }
@@ -62,7 +75,7 @@ __global__ void __launch_bounds__(32 * kEmbWarps) embedding_kernel(EmbeddingArgs
             __syncwarp();
         }
 #pragma unroll
-        for (int u = 0; u < kEmbSpans; ++u) {
+        for (int u = 0; u < kEmbSpans<S, D>; ++u) {
             if (u * kSpan >= left) break;
             const int64_t g = g0 + u * 32;
             if constexpr (!kAligned)
@@ -106,7 +119,7 @@ constexpr int kMaxBits = 9;      // of a digit: the counts of 32 warps take half
 constexpr int kSortCluster = 8;
 constexpr int kKeep = 8;         // tokens of a lane at a time
 constexpr int kTile = kSortThreads * kKeep;
-constexpr int kFewTokens = 512;  // ranked by comparisons
+constexpr int kFewTokens = 512;  // summed without a sort
 
 // A row whose tokens lie in chunks first, first + 1, ..., first + more.
 struct Crossing {
@@ -376,42 +389,6 @@ __global__ void __launch_bounds__(kSortThreads)
     cluster_sync();  // no block leaves while another reads its counts
 }
 
-// The same for up to kFewTokens tokens, one block: a token's place is the
-// number of tokens that come before it.
-__global__ void __launch_bounds__(2 * kFewTokens) embedding_few_kernel(EmbeddingGradArgs a, GradWork w) {
-    __shared__ int4 keys[kFewTokens / 4];
-    __shared__ int place[kFewTokens], named;
-    allow_next();
-    // two threads a token, each for half of the others
-    const int tid = threadIdx.x % kFewTokens, half = threadIdx.x / kFewTokens, n = (int)a.n, quads = (n + 3) / 4;
-    const int row = tid < n ? row_of(read_id(a.ids, a.wide_ids, tid), a.first, a.vocab) : 0x7fffffff;
-    if (half == 0) {
-        reinterpret_cast<int*>(keys)[tid] = row;
-        place[tid] = 0;
-    }
-    if (threadIdx.x == 0) {
-        named = 0;
-        *w.crossings = 0;
-    }
-    if (!a.accumulate)
-        for (int64_t i = threadIdx.x; i < (a.vocab + 31) / 32; i += 2 * kFewTokens) w.marks[i] = 0;
-    __syncthreads();
-    if (tid < n) {
-        int before = 0;
-#pragma unroll 4
-        for (int j = half * (quads / 2); j < (half ? quads : quads / 2); ++j) {
-            const int4 k = keys[j];
-            before += (k.x < row || (k.x == row && 4 * j < tid)) + (k.y < row || (k.y == row && 4 * j + 1 < tid)) +
-                      (k.z < row || (k.z == row && 4 * j + 2 < tid)) + (k.w < row || (k.w == row && 4 * j + 3 < tid));
-        }
-        atomicAdd(&place[tid], before);
-        if (half == 0 && row < a.vocab) atomicAdd(&named, 1);
-    }
-    __syncthreads();
-    if (half == 0 && tid < n) w.sorted[0][place[tid]] = make_int2(row, tid);
-    if (threadIdx.x == 0) *w.count = named;
-}
-
 // ------------------------------------------------------------ gradient: zeros and sums
 
 // Scales a row's sums, adds what the table holds where the caller wants it,
@@ -472,18 +449,32 @@ __device__ __forceinline__ void zero_row(D* row, int64_t n, int lane) {
     for (uintptr_t q = body + lane * 16; q < tail; q += 512) st_stream(reinterpret_cast<uint4*>(q), make_uint4(0, 0, 0, 0));
 }
 
+// Zeros for the columns from first on (width of them) of those of count rows
+// from r0 on that have no bit in named. Neighbouring rows without a gap between
+// them are one stretch.
+template <typename D>
+__device__ __forceinline__ void zero_rows(const EmbeddingGradArgs& a, int64_t r0, int count, uint32_t named, int64_t first,
+                                          int64_t width, int lane) {
+    uint32_t todo = ~named & (count < 32 ? (1u << count) - 1 : ~0u);
+    while (todo) {
+        const int i = __ffs(todo) - 1;
+        const uint32_t past = ~(todo >> i);
+        const int run = a.table.stride == width && past ? __ffs(past) - 1 : (a.table.stride == width ? 32 - i : 1);
+        zero_row(static_cast<D*>(a.table.data) + (r0 + i) * a.table.stride + first, run * width, lane);
+        todo &= run < 32 ? ~(((1u << run) - 1) << i) : 0u;
+    }
+}
+
 // Block z writes the zeros of its rows, per for each warp (a power of two up to
-// 32, so that their marks lie in one word), that are not marked; marks NULL:
-// none is. Many short blocks: 131072 rows of 32 KB take 575 us in blocks of 8
-// rows and 656 in two blocks an SM that each take a long range.
+// 32, so that their marks lie in one word), that are not marked. Many short
+// blocks: 131072 rows of 32 KB take 575 us in blocks of 8 rows and 656 in two
+// blocks an SM that each take a long range.
 template <typename D>
 __device__ __forceinline__ void write_zeros(const EmbeddingGradArgs& a, const uint32_t* marks, int64_t z, int per) {
-    const int lane = threadIdx.x & 31;
     const int64_t r0 = (z * kEmbWarps + (threadIdx.x >> 5)) * per;
     if (r0 >= a.vocab) return;
-    const uint32_t named = marks ? __ldcg(marks + (r0 >> 5)) >> (r0 & 31) : 0u;
-    for (int i = 0; i < per && r0 + i < a.vocab; ++i)
-        if (!(named >> i & 1)) zero_row(static_cast<D*>(a.table.data) + (r0 + i) * a.table.stride, a.cols, lane);
+    const uint32_t named = __ldcg(marks + (r0 >> 5)) >> (r0 & 31);
+    zero_rows<D>(a, r0, (int)(a.vocab - r0 < per ? a.vocab - r0 : per), named, 0, a.cols, threadIdx.x & 31);
 }
 
 // Tokens whose gradients a warp has in flight, in shared memory.
@@ -584,7 +575,7 @@ __global__ void __launch_bounds__(32 * kEmbWarps) embedding_join_kernel(Embeddin
     __shared__ float4 sums[kEmbWarps][2][32];
     wait_for_previous();
     if ((int)blockIdx.x >= spans * ys) {
-        write_zeros<D>(a, w.nchunks ? w.marks : nullptr, blockIdx.x - spans * ys, per);
+        write_zeros<D>(a, w.marks, blockIdx.x - spans * ys, per);
         return;
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, y = blockIdx.x / spans;
@@ -615,13 +606,161 @@ __global__ void __launch_bounds__(32 * kEmbWarps) embedding_join_kernel(Embeddin
     }
 }
 
+// -------------------------------------------- gradient: up to kFewTokens tokens
+
+// Adds to acc the gradients of the listed tokens for the 256 columns from c0
+// on (left of them), kFlight in flight.
+template <typename S, bool kAligned>
+__device__ __forceinline__ Cols sum_tokens(const EmbeddingGradArgs& a, const short* list, int m, int64_t c0, int left, uint4* slots,
+                                           int lane) {
+    constexpr int kOne = kSlot<kAligned, S>;
+    auto gradient = [&](int j) { return static_cast<const S*>(a.grad.data) + list[j] * a.grad.stride + c0; };
+    auto fetch = [&](int j) {
+        if (j < m) span_fetch<kAligned>(slots + j % kFlight * kOne, gradient(j), 0, left, lane);
+        async_commit();
+    };
+    Cols acc = all(0.0f);
+    for (int j = 0; j < kFlight - 1; ++j) fetch(j);
+#pragma unroll 1
+    for (int j = 0; j < m; ++j) {
+        fetch(j + kFlight - 1);
+        async_wait<kFlight - 1>();
+        __syncwarp();
+        Raw<S> in;
+        span_read<kAligned>(in, slots + j % kFlight * kOne, gradient(j), 0, lane);
+        acc = acc + widened(in);
+        __syncwarp();  // before the slot is filled again
+    }
+    return acc;
+}
+
+// One kernel and no sort: every block holds all tokens' rows, and a warp looks
+// for those of its own `per` rows among them, for a group of kGroup spans of
+// columns (blockIdx.y). It writes zeros, or sums up to kAlone tokens by itself;
+// rows of more tokens are left for the whole block, its warps taking a span
+// and a share of the tokens each. (Groups of 4 spans: 300 tokens, most in three
+// rows of 1027, 17 us instead of 12; of 1 span, 32000 x 4096 takes 64 us
+// instead of 42.)
+constexpr int kAlone = 8, kGroup = 2;
+template <typename S, typename D, bool kAligned>
+__global__ void __launch_bounds__(32 * kEmbWarps)
+    embedding_few_kernel(EmbeddingGradArgs a, int per) {
+    extern __shared__ uint4 flight[];
+    __shared__ int keys[kFewTokens];
+    __shared__ short list[kEmbWarps][kAlone], shared_list[kFewTokens];
+    __shared__ int64_t many[kEmbWarps * 32];
+    __shared__ int manies, found;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = (int)a.n, quads = (n + 31) / 32;
+    constexpr int kMine = kFlight * kSlot<kAligned, S>;
+    uint4* const slots = flight + warp * kMine;
+    const int64_t first = (int64_t)blockIdx.y * (kGroup * kSpan);
+    const int width = (int)(a.cols - first < kGroup * kSpan ? a.cols - first : kGroup * kSpan), spans = (width + kSpan - 1) / kSpan;
+    for (int i = threadIdx.x; i < quads * 32; i += 32 * kEmbWarps)
+        keys[i] = i < n ? row_of(read_id(a.ids, a.wide_ids, i), a.first, a.vocab) : -1;
+    if (threadIdx.x == 0) manies = 0;
+    __syncthreads();
+    // the sums of a span of the group, and their store
+    auto sum = [&](const short* tokens, int m, int s) {
+        const int left = width - s * kSpan < kSpan ? width - s * kSpan : kSpan;
+        return sum_tokens<S, kAligned>(a, tokens, m, first + s * kSpan, left, slots, lane);
+    };
+    auto store = [&](int64_t row, int s, const Cols& acc) {
+        store_row<D, kAligned>(a, (int)row, (first / kSpan + s) * 32 + lane, acc, lane);
+    };
+
+    const int64_t r0 = ((int64_t)blockIdx.x * kEmbWarps + warp) * per;
+    if (r0 < a.vocab) {
+        // which of the warp's rows are named
+        uint32_t named = 0;
+        for (int q = 0; q < quads; ++q) {
+            const uint32_t at = (uint32_t)keys[q * 32 + lane] - (uint32_t)r0;
+            if (at < (uint32_t)per) named |= 1u << at;
+        }
+        named = __reduce_or_sync(kFull, named);
+        const int rows = (int)(a.vocab - r0 < per ? a.vocab - r0 : per);
+        if (!a.accumulate) zero_rows<D>(a, r0, rows, named, first, width, lane);
+        for (int i = 0; i < rows; ++i) {
+            const int64_t row = r0 + i;
+            if (!(named >> i & 1)) continue;
+            int m = 0;  // its tokens, in ascending order
+            for (int q = 0; q < quads; ++q) {
+                const unsigned hit = __ballot_sync(kFull, keys[q * 32 + lane] == (int)row);
+                const int at = m + __popc(hit & ((1u << lane) - 1));
+                if ((hit >> lane & 1) && at < kAlone) list[warp][at] = (short)(q * 32 + lane);
+                m += __popc(hit);
+            }
+            __syncwarp();
+            if (m > kAlone) {
+                if (lane == 0) many[atomicAdd(&manies, 1)] = row;
+                continue;
+            }
+            for (int s = 0; s < spans; ++s) store(row, s, sum(list[warp], m, s));
+            __syncwarp();
+        }
+    }
+    __syncthreads();
+    const int count = manies, shares = kEmbWarps / spans;
+    for (int k = 0; k < count; ++k) {
+        const int64_t row = many[k];
+        if (warp == 0) {
+            int m = 0;
+            for (int q = 0; q < quads; ++q) {
+                const unsigned hit = __ballot_sync(kFull, keys[q * 32 + lane] == (int)row);
+                if (hit >> lane & 1) shared_list[m + __popc(hit & ((1u << lane) - 1))] = (short)(q * 32 + lane);
+                m += __popc(hit);
+            }
+            if (lane == 0) found = m;
+        }
+        __syncthreads();
+        const int m = found;
+        const int share = warp / spans, s = warp - share * spans;
+        Cols acc = all(0.0f);
+        if (share < shares) {
+            const int j0 = m * share / shares, j1 = m * (share + 1) / shares;
+            acc = sum(shared_list + j0, j1 - j0, s);
+            store_part(reinterpret_cast<float*>(slots + 2 * lane), acc);  // what was in flight has been read
+        }
+        __syncthreads();
+        if (share == 0) {
+            for (int q = 1; q < shares; ++q) {
+                const float4* other = reinterpret_cast<const float4*>(slots + q * spans * kMine + 2 * lane);
+                const float4 u = other[0], v = other[1];
+                acc = acc + Cols{{make_float2(u.x, u.y), make_float2(u.z, u.w), make_float2(v.x, v.y), make_float2(v.z, v.w)}};
+            }
+            store(row, s, acc);
+        }
+        __syncthreads();
+    }
+}
+
+template <typename S, typename D, bool kAligned>
+cudaError_t embedding_grad_few(const EmbeddingGradArgs& a, cudaStream_t s) {
+    const int64_t groups = (a.cols + kGroup * kSpan - 1) / (kGroup * kSpan), width = groups > 1 ? kGroup * kSpan : a.cols;
+    if (groups > 65535) return cudaErrorInvalidValue;
+    int per = 1;
+    while (per < 32 && 2 * per * width * (int64_t)sizeof(D) <= 8192) per *= 2;
+    const int64_t blocks = (a.vocab + per * kEmbWarps - 1) / (per * kEmbWarps);
+    constexpr int smem = kEmbWarps * kFlight * kSlot<kAligned, S> * 16;
+    static std::atomic<uint64_t> done{0};
+    auto kernel = embedding_few_kernel<S, D, kAligned>;
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), smem, done);
+    if (e != cudaSuccess) return e;
+    kernel<<<dim3((unsigned)blocks, (unsigned)groups), 32 * kEmbWarps, smem, s>>>(a, per);
+    count_launch();
+    return cudaGetLastError();
+}
+
 template <typename S, typename D, bool kAligned>
 cudaError_t embedding_grad_as(const EmbeddingGradArgs& a, cudaStream_t s) {
+    // One kernel against three: 64 tokens into 32000 x 4096 bf16 38 and 49 us,
+    // 300 into 4099 x 1027 fp32, nine in ten of them in three rows, 12 and 20,
+    // spread 9 and 21. With many tokens a row it falls behind, a block having
+    // a row's tokens to itself: 512 into 7 rows of 8192 45 and 16.
+    if (a.n <= kFewTokens && a.n <= 8 * a.vocab) return embedding_grad_few<S, D, kAligned>(a, s);
     const GradWork w = grad_work(a.work, a.n, a.vocab, a.cols, nullptr);
     int need = 1;
     while (((int64_t)1 << need) <= a.vocab) ++need;  // bits of the values 0 .. vocab
-    const bool few = a.n <= kFewTokens;
-    const int passes = few ? 1 : (need + kMaxBits - 1) / kMaxBits, bits = (need + passes - 1) / passes;
+    const int passes = (need + kMaxBits - 1) / kMaxBits, bits = (need + passes - 1) / passes;
     const int spans = (int)((a.cols + kSpan - 1) / kSpan);
     const int64_t sums = (w.nchunks * (int64_t)spans + kEmbWarps - 1) / kEmbWarps;
     // a warp of zeros takes one row, or more that make up 8 KB
@@ -631,11 +770,7 @@ cudaError_t embedding_grad_as(const EmbeddingGradArgs& a, cudaStream_t s) {
     const int ys = w.nchunks <= 1 ? 0 : (w.nchunks - 1 < 64 ? w.nchunks - 1 : 64);
     if (sums > 0x7fffffff || zeros + (int64_t)spans * ys > 0x7fffffff) return cudaErrorInvalidValue;
     cudaError_t e = cudaSuccess;
-    if (few && a.n > 0) {
-        embedding_few_kernel<<<1, 2 * kFewTokens, 0, s>>>(a, w);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        count_launch();
-    } else if (a.n > 0) {
+    {
         const size_t smem = SortSmem::bytes(1 << bits);
         static std::atomic<uint64_t> done{0};
         e = allow_smem(reinterpret_cast<const void*>(embedding_sort_kernel), (int)SortSmem::bytes(1 << kMaxBits), done);
@@ -655,7 +790,7 @@ cudaError_t embedding_grad_as(const EmbeddingGradArgs& a, cudaStream_t s) {
         count_launch();
     }
     const int2* const sorted = w.sorted[(passes - 1) & 1];
-    if (a.n > 0) {
+    {
         constexpr int smem = kEmbWarps * kFlight * kSlot<kAligned, S> * 16;
         static std::atomic<uint64_t> done{0};
         auto kernel = embedding_sum_kernel<S, D, kAligned>;
@@ -664,14 +799,8 @@ cudaError_t embedding_grad_as(const EmbeddingGradArgs& a, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         count_launch();
     }
-    const dim3 grid((unsigned)(zeros + spans * ys));
-    if (grid.x == 0) return cudaSuccess;
-    if (a.n > 0) {
-        e = launch_next(embedding_join_kernel<D, kAligned>, grid, 32 * kEmbWarps, 0, s, a, w, spans, ys, per);
-    } else {  // nothing of this call before it
-        embedding_join_kernel<D, kAligned><<<grid, 32 * kEmbWarps, 0, s>>>(a, w, spans, ys, per);
-        e = cudaGetLastError();
-    }
+    if (zeros + spans * ys == 0) return cudaSuccess;
+    e = launch_next(embedding_join_kernel<D, kAligned>, dim3((unsigned)(zeros + spans * ys)), 32 * kEmbWarps, 0, s, a, w, spans, ys, per);
     if (e == cudaSuccess) count_launch();
     return e;
 }
@@ -684,7 +813,7 @@ cudaError_t embedding_grad(const EmbeddingGradArgs& a, cudaStream_t s) {
 
 template <typename S, typename D>
 cudaError_t embedding(const EmbeddingArgs& a, cudaStream_t s) {
-    const int64_t spans = (a.cols + kSpan - 1) / kSpan, steps = (spans + kEmbSpans - 1) / kEmbSpans, items = steps * a.n;
+    const int64_t spans = (a.cols + kSpan - 1) / kSpan, steps = (spans + kEmbSpans<S, D> - 1) / kEmbSpans<S, D>, items = steps * a.n;
     const int per = (int)((spans + steps - 1) / steps);
     const int64_t blocks = (items + kEmbWarps - 1) / kEmbWarps;
     const unsigned grid = (unsigned)(blocks < 0x7fffffff ? blocks : 0x7fffffff);
