@@ -736,7 +736,6 @@ __global__ void __launch_bounds__(32 * kEmbWarps)
 template <typename S, typename D, bool kAligned>
 cudaError_t embedding_grad_few(const EmbeddingGradArgs& a, cudaStream_t s) {
     const int64_t groups = (a.cols + kGroup * kSpan - 1) / (kGroup * kSpan), width = groups > 1 ? kGroup * kSpan : a.cols;
-    if (groups > 65535) return cudaErrorInvalidValue;
     int per = 1;
     while (per < 32 && 2 * per * width * (int64_t)sizeof(D) <= 8192) per *= 2;
     const int64_t blocks = (a.vocab + per * kEmbWarps - 1) / (per * kEmbWarps);
@@ -756,7 +755,8 @@ cudaError_t embedding_grad_as(const EmbeddingGradArgs& a, cudaStream_t s) {
     // 300 into 4099 x 1027 fp32, nine in ten of them in three rows, 12 and 20,
     // spread 9 and 21. With many tokens a row it falls behind, a block having
     // a row's tokens to itself: 512 into 7 rows of 8192 45 and 16.
-    if (a.n <= kFewTokens && a.n <= 8 * a.vocab) return embedding_grad_few<S, D, kAligned>(a, s);
+    if (a.n <= kFewTokens && a.n <= 8 * a.vocab && a.cols <= (int64_t)65535 * kGroup * kSpan)
+        return embedding_grad_few<S, D, kAligned>(a, s);
     const GradWork w = grad_work(a.work, a.n, a.vocab, a.cols, nullptr);
     int need = 1;
     while (((int64_t)1 << need) <= a.vocab) ++need;  // bits of the values 0 .. vocab

@@ -128,7 +128,8 @@ GRAD_KINDS = ["uniform", "hot", "one", "none", "wild", "sorted"]
 @pytest.mark.parametrize("n, vocab, cols, gdt, tdt", [
     (1, 1, 1, "f32", "f32"), (31, 4, 8, "bf16", "bf16"), (32, 50, 256, "bf16", "f32"), (33, 300, 257, "f32", "bf16"),
     (300, 4099, 67, "f32", "f32"), (1025, 70, 130, "bf16", "bf16"), (2100, 256, 264, "bf16", "f32"), (700, 65535, 9, "f32", "f32"),
-    (5000, 3, 40, "f32", "f32")])
+    (5000, 3, 40, "f32", "f32"), (300, 50, 1300, "bf16", "f32"), (512, 64, 513, "f32", "f32"), (513, 70, 1300, "f32", "bf16"),
+    (512, 63, 24, "bf16", "bf16")])
 def test_embedding_grad(kind, n, vocab, cols, gdt, tdt):
     grad = rand(4, n, cols, NAMES[gdt], pad=(3 if cols % 2 else 8) * (n % 2))
     ids = ids_of(5, n, vocab, kind, torch.int32 if n % 2 else torch.int64)
@@ -151,7 +152,8 @@ def test_embedding_grad(kind, n, vocab, cols, gdt, tdt):
 
 
 @pytest.mark.parametrize("n, vocab, kind", [(20000, 17, "uniform"), (9000, 40000, "hot"), (40000, 1000, "one"), (8193, 2 ** 17 + 5, "uniform"),
-                                            (100003, 131, "wild"), (20000, 70000, "sorted")])
+                                            (100003, 131, "wild"), (20000, 70000, "sorted"), (9000, 2 ** 19 + 3, "uniform"),
+                                            (4097, 250, "hot"), (512, 100000, "hot")])
 def test_embedding_grad_of_many_tokens_is_exact_on_whole_numbers(n, vocab, kind):
     # sums of small whole numbers are exact in any order: what is checked is
     # that every token reaches its row once, across the sort's blocks and the
@@ -207,7 +209,7 @@ def test_embedding_gradient_against_differences():
 
 # ----------------------------------------------------------------- dropout
 
-SIZES = [(1, 1, 0, 0), (3, 8, 0, 0), (5, 7, 0, 0), (2, 256, 0, 0), (37, 1000, 0, 0), (4, 511, 1, 3), (9, 2056, 8, 0), (130, 33, 0, 1),
+SIZES = [(700, 512, 0, 0), (90, 520, 0, 0), (600, 97, 0, 0), (1, 1, 0, 0), (3, 8, 0, 0), (5, 7, 0, 0), (2, 256, 0, 0), (37, 1000, 0, 0), (4, 511, 1, 3), (9, 2056, 8, 0), (130, 33, 0, 1),
          (1, 70001, 0, 0)]
 
 
@@ -287,6 +289,33 @@ def test_dropout_of_a_tensor_of_three_dimensions():
 NORM_SIZES = [(1, 1, 0, 0), (3, 2, 0, 0), (5, 8, 0, 0), (9, 100, 0, 0), (33, 256, 8, 0), (4, 513, 0, 1), (7, 1024, 0, 0), (6, 1537, 1, 3),
               (3, 4096, 0, 0), (2, 5003, 0, 0), (3, 8192, 0, 0), (2, 16384, 0, 0), (2, 16391, 0, 0), (1, 40000, 0, 0), (700, 72, 0, 0)]
 MODES = [(0.0, False), (0.0, True), (0.1, False), (0.25, True)]
+
+
+# more rows than the GPU holds at once, for every number of granules a thread
+MANY_ROWS = [(6000, 40, 0, 0), (5003, 201, 0, 1), (2000, 520, 0, 0), (400, 1000, 0, 0), (400, 1001, 0, 0), (380, 2500, 0, 0), (401, 4096, 8, 0),
+             (310, 5003, 0, 0), (320, 8192, 0, 0), (310, 9000, 0, 0)]
+
+
+@pytest.mark.parametrize("rows, cols, pad, offset", MANY_ROWS)
+@pytest.mark.parametrize("dt", NAMES)
+def test_layer_norm_of_many_rows(dt, rows, cols, pad, offset):
+    x, res = rand(1, rows, cols, NAMES[dt], pad=pad, offset=offset), rand(2, rows, cols, NAMES[dt], pad=pad)
+    w, b = vec(3, cols, NAMES[dt], 1.0), vec(4, cols, NAMES[dt])
+    out, hid = Guarded(rows, cols, NAMES[dt], pad, offset), Guarded(rows, cols, NAMES[dt], pad, 0)
+    mean, rstd = Guarded(1, rows, F32), Guarded(1, rows, F32)
+    C.fsdp_layer_norm(x, w, b, out.t, mean.t, rstd.t, residual=res, hidden=hid.t, p=0.1, seed=21, draw=1)
+    want = R.layer_norm(x, w, b, 1e-5, res, 0.1, 21, 1)
+    for name, got in (("out", out), ("hidden", hid), ("mean", mean), ("rstd", rstd)):
+        R.agree(name, got.check(), want[name])
+    gx, gr = Guarded(rows, cols, NAMES[dt], pad, offset), Guarded(rows, cols, NAMES[dt], pad, 0)
+    gw, gb = Guarded(1, cols, F32), Guarded(1, cols, F32)
+    work = Workspace(C.fsdp_layer_norm_grad_workspace(rows, cols))
+    C.fsdp_layer_norm_grad(x, hid.t, mean.t.view(-1), rstd.t.view(-1), w, gx.t, gw.t.view(-1), gb.t.view(-1), work.t, grad_hidden=res,
+                           grad_residual=gr.t, p=0.1, seed=21, draw=1)
+    work.check()
+    want = R.layer_norm_grad(x, hid.t, mean.t.view(-1), rstd.t.view(-1), w, F32, res, 0.1, 21, 1)
+    for name, got in (("grad_x", gx), ("grad_residual", gr), ("grad_weight", gw), ("grad_bias", gb)):
+        R.agree(name, got.check(), want[name])
 
 
 @pytest.mark.parametrize("dt, pdt", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32"), ("f32", "bf16")])

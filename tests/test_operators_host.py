@@ -123,6 +123,7 @@ def test_workspace_queries():
     b = ctypes.c_size_t()
     refused(C.lib().fsdp_embedding_grad_workspace(-1, 4, 8, ctypes.byref(b)))
     refused(C.lib().fsdp_embedding_grad_workspace(1, 4, 8, None), "NULL")
+    refused(C.lib().fsdp_embedding_grad_workspace(1, 4, 2 ** 31, ctypes.byref(b)), "columns")
     refused(C.lib().fsdp_layer_norm_grad_workspace(1, -8, ctypes.byref(b)))
     assert C.fsdp_layer_norm_grad_workspace(0, 100) == 0
     # no more than a few times what the operators read
