@@ -397,9 +397,11 @@ int fsdp_rs_ar_reduce_noalloc(fsdp_plan_t plan, int grad_dtype, const void* cons
  * have no counterpart; the operators exist for this library's users. They
  * need no plan, work on the current device, and follow the conventions at
  * the head of this file, except that a backward pass enqueues up to three
- * kernels and takes its scratch memory from the caller: a device buffer,
- * 16-byte aligned, of the size its _workspace function gives; calls that may
- * overlap on the GPU need workspaces of their own. Nothing in a workspace is
+ * kernels, each of which may be launched while the one before it runs (a
+ * programmatic dependent launch, which also a captured graph keeps), and takes
+ * its scratch memory from the caller: a device buffer, 16-byte aligned, of the
+ * size its _workspace function gives; calls that may overlap on the GPU need
+ * workspaces of their own. Nothing in a workspace is
  * read before it is written, and nothing is kept there between calls.
  *
  * Matrices: element (r, c) sits at data[r * stride + c]; strides count
@@ -412,7 +414,8 @@ int fsdp_rs_ar_reduce_noalloc(fsdp_plan_t plan, int grad_dtype, const void* cons
  *
  * Numerics: everything between an operator's inputs and outputs is computed
  * and summed in binary32 and rounded once to the output's type. Sums are
- * taken in an order fixed by the sizes, so equal calls give equal bits. A
+ * taken in an order fixed by the sizes and the GPU's number of SMs, so equal
+ * calls give equal bits. A
  * result that is not a number is some NaN. */
 
 enum fsdp_index_type { FSDP_I32 = 0, FSDP_I64 = 1 };

@@ -462,8 +462,9 @@ def test_strides_past_32_bits():
     R.agree("grad", out, R.embedding_grad(y.t, ids, 2, 1.0, 0, BF16))
 
 
-def test_side_stream_and_graph():
-    n, vocab, cols = 500, 80, 136
+@pytest.mark.parametrize("n", [500, 3000, 9000])  # the gradient in one kernel, and by a sort of one and of several blocks
+def test_side_stream_and_graph(n):
+    vocab, cols = 80, 136
     table, ids = rand(1, vocab, cols, BF16), ids_of(2, n, vocab, "uniform")
     w, b = vec(3, cols, BF16, 1.0), vec(4, cols, BF16)
     new = lambda *s, dtype=BF16: torch.empty(*s, dtype=dtype, device="cuda")  # noqa: E731
