@@ -143,10 +143,12 @@ struct GradWork {
 int64_t up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
 
 // Tokens of a chunk: few while that gives no more warps than the GPU holds at
-// once (the fewer, the sooner the longest is done), else 32.
+// once (the fewer, the sooner the longest is done) and no long lists of parts
+// for rows of many tokens (57970 tokens, most in three rows of 16 columns: 84 us
+// with chunks of 8, 49 with 32), else 32.
 int chunk_tokens(int64_t n, int64_t cols) {
     const int64_t spans = (cols + kSpan - 1) / kSpan, warps = 64 * (int64_t)sm_count();
-    return n * spans <= 8 * warps ? 8 : (n * spans <= 16 * warps ? 16 : 32);
+    return n <= 4096 && n * spans <= 8 * warps ? 8 : (n <= 16384 && n * spans <= 16 * warps ? 16 : 32);
 }
 
 GradWork grad_work(void* work, int64_t n, int64_t vocab, int64_t cols, size_t* bytes) {
@@ -553,11 +555,18 @@ __global__ void __launch_bounds__(32 * kEmbWarps, sizeof(S) == 4 ? 3 : 5)
 }
 
 // The sum of a crossing row's parts p0 ... p1 - 1: the first chunk's tail, then
-// what the others leave at their heads.
-__device__ __forceinline__ Cols sum_parts(const GradWork& w, const int4& x, int p0, int p1, int64_t c) {
+// what the others leave at their heads. Where a row has few granules, `wide`
+// lanes (a power of two) hold it and the warp adds 32 / wide parts at a time;
+// all lanes take part, and every wide of them get the sum.
+__device__ __forceinline__ Cols sum_parts(const GradWork& w, const int4& x, int p0, int p1, int64_t c, bool on, int wide, int lane) {
     Cols acc = all(0.0f);
-#pragma unroll 4
-    for (int p = p0; p < p1; ++p) acc = acc + load_part(w.part + (x.y + p + (p == 0 ? w.nchunks : 0)) * w.stride + c);
+    if (on)
+#pragma unroll 8
+        for (int p = p0 + lane / wide; p < p1; p += 32 / wide)
+            acc = acc + load_part(w.part + (x.y + p + (p == 0 ? w.nchunks : 0)) * w.stride + c);
+    for (int d = wide; d < 32; d *= 2)
+#pragma unroll
+        for (int e = 0; e < kGran; ++e) acc.set(e, acc.get(e) + __shfl_xor_sync(kFull, acc.get(e), d));
     return acc;
 }
 
@@ -571,7 +580,7 @@ __device__ __forceinline__ bool sound(const EmbeddingGradArgs& a, const GradWork
 // other blocks write zeros.
 constexpr int kShort = 8;
 template <typename D, bool kAligned>
-__global__ void __launch_bounds__(32 * kEmbWarps) embedding_join_kernel(EmbeddingGradArgs a, GradWork w, int spans, int ys, int per) {
+__global__ void __launch_bounds__(32 * kEmbWarps) embedding_join_kernel(EmbeddingGradArgs a, GradWork w, int spans, int ys, int per, int wide) {
     __shared__ float4 sums[kEmbWarps][2][32];
     wait_for_previous();
     if ((int)blockIdx.x >= spans * ys) {
@@ -579,19 +588,19 @@ __global__ void __launch_bounds__(32 * kEmbWarps) embedding_join_kernel(Embeddin
         return;
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, y = blockIdx.x / spans;
-    const int64_t g = (int64_t)(blockIdx.x - y * spans) * 32 + lane, c = g * kGran;
-    const int n = granule_cols(g, a.cols);
+    const int64_t g = (int64_t)(blockIdx.x - y * spans) * 32 + lane, c = (g - lane + lane % wide) * kGran;
+    const bool on = c < a.cols;
     const int crossings = min(__ldcg(w.crossings), w.nchunks);
     for (int i = y * kEmbWarps + warp; i < crossings; i += ys * kEmbWarps) {
         const int4 x = __ldcg(reinterpret_cast<const int4*>(w.cross + i));
         if (x.z >= kShort || !sound(a, w, x)) continue;
-        store_row<D, kAligned>(a, x.x, g, n ? sum_parts(w, x, 0, x.z + 1, c) : all(0.0f), lane);
+        store_row<D, kAligned>(a, x.x, g, sum_parts(w, x, 0, x.z + 1, c, on, wide, lane), lane);
     }
     for (int i = y; i < crossings; i += ys) {
         const int4 x = __ldcg(reinterpret_cast<const int4*>(w.cross + i));
         const int parts = x.z + 1;
         if (parts <= kShort || !sound(a, w, x)) continue;
-        Cols acc = n ? sum_parts(w, x, parts * warp / kEmbWarps, parts * (warp + 1) / kEmbWarps, c) : all(0.0f);
+        Cols acc = sum_parts(w, x, parts * warp / kEmbWarps, parts * (warp + 1) / kEmbWarps, c, on, wide, lane);
         sums[warp][0][lane] = make_float4(acc.p[0].x, acc.p[0].y, acc.p[1].x, acc.p[1].y);
         sums[warp][1][lane] = make_float4(acc.p[2].x, acc.p[2].y, acc.p[3].x, acc.p[3].y);
         __syncthreads();
@@ -768,6 +777,8 @@ cudaError_t embedding_grad_as(const EmbeddingGradArgs& a, cudaStream_t s) {
     while (per < 32 && 2 * per * a.cols * (int64_t)sizeof(D) <= 8192) per *= 2;
     const int64_t zeros = a.accumulate ? 0 : (a.vocab + per * kEmbWarps - 1) / (per * kEmbWarps);
     const int ys = w.nchunks <= 1 ? 0 : (w.nchunks - 1 < 64 ? w.nchunks - 1 : 64);
+    int wide = 32;  // lanes of a row's granules in the joins
+    while (wide > 1 && (wide / 2) * kGran >= a.cols) wide /= 2;
     if (sums > 0x7fffffff || zeros + (int64_t)spans * ys > 0x7fffffff) return cudaErrorInvalidValue;
     cudaError_t e = cudaSuccess;
     {
@@ -800,7 +811,7 @@ cudaError_t embedding_grad_as(const EmbeddingGradArgs& a, cudaStream_t s) {
         count_launch();
     }
     if (zeros + spans * ys == 0) return cudaSuccess;
-    e = launch_next(embedding_join_kernel<D, kAligned>, dim3((unsigned)(zeros + spans * ys)), 32 * kEmbWarps, 0, s, a, w, spans, ys, per);
+    e = launch_next(embedding_join_kernel<D, kAligned>, dim3((unsigned)(zeros + spans * ys)), 32 * kEmbWarps, 0, s, a, w, spans, ys, per, wide);
     if (e == cudaSuccess) count_launch();
     return e;
 }
