@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(32 * kEmbWarps) embedding_kernel(EmbeddingArgs
             if constexpr (kAligned)
                 load_table(in[u], from, (g0 + u * 32) * kGran, granule_cols(g0 + u * 32, a.cols));
             else
-                span_fetch<false>(mine[u], from + c0, u * kSpan, left, lane);
+                span_fetch<false, true>(mine[u], from + c0, u * kSpan, left, lane);  // rows are looked up again
         }
         if constexpr (!kAligned) {
             async_commit();

@@ -278,9 +278,14 @@ __device__ __forceinline__ void cut(Cols& x, int n) {
 template <bool kAligned, typename T>
 constexpr int kSlot = 32 * Raw<T>::kVec + (kAligned ? 0 : 1);
 
+// kCached: through the L1 cache, for what an SM reads again.
+template <bool kCached>
 __device__ __forceinline__ void async_copy(uint4* dst, uintptr_t src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
-                 : "memory");
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+    if constexpr (kCached)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
 }
 __device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kLeft>
@@ -290,7 +295,7 @@ __device__ __forceinline__ void async_wait() {
 
 // Starts the copies of the 16-byte blocks that hold a row's columns c0 ...
 // c0 + 255; no block that lies wholly past the row's end is touched.
-template <bool kAligned, typename T>
+template <bool kAligned, bool kCached = false, typename T>
 __device__ __forceinline__ void span_fetch(uint4* slot, const T* row, int c0, int cols, int lane) {
     constexpr int kV = Raw<T>::kVec;
     const uintptr_t from = reinterpret_cast<uintptr_t>(row + c0);
@@ -299,7 +304,7 @@ __device__ __forceinline__ void span_fetch(uint4* slot, const T* row, int c0, in
 #pragma unroll
     for (int v = 0; v < kV + (kAligned ? 0 : 1); ++v) {
         const int b = v * 32 + lane;
-        if ((v < kV || lane == 0) && b * 16 < bytes) async_copy(slot + b, from - sh + b * 16);
+        if ((v < kV || lane == 0) && b * 16 < bytes) async_copy<kCached>(slot + b, from - sh + b * 16);
     }
 }
 
