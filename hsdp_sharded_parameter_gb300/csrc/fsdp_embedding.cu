@@ -4,7 +4,8 @@
 // no row.
 //
 // Gradient: grad_table[v] = scale * sum of grad_out[t] over the tokens t of
-// row v. One kernel for few tokens (below); else three, each launched while the one before it runs:
+// row v. One kernel for few tokens (below); else three, each launched while the
+// one before it runs:
 //   1. a stable radix sort of (row, token) by one cluster of blocks;
 //   2. sums: a warp adds up the gradients of a chunk of sorted tokens for a
 //      span of 256 columns, writes the rows that lie inside the chunk, leaves
@@ -357,7 +358,8 @@ __device__ __forceinline__ void sort_pass(const EmbeddingGradArgs& a, const Sort
             if (i < hi - b) {
                 const int2 x = sm.tile[i];
                 const int d = (x.x >> shift) & (bins - 1);
-                out[sm.base[d] + i - sm.start[d]] = x;
+                const uint32_t at = sm.base[d] + i - sm.start[d];
+                if (at < (uint32_t)n) out[at] = x;  // always, but in a workspace that another call shares
             }
         }
         if (one) break;
@@ -502,7 +504,7 @@ __global__ void __launch_bounds__(32 * kEmbWarps, sizeof(S) == 4 ? 3 : 5)
     // (calls that shared a workspace in spite of the header would leave any
     // numbers there: no gradient, row or part outside its matrix is touched)
     int2 mine = lane < m ? __ldcg(sorted + lo + lane) : make_int2(-1, 0);
-    mine = make_int2(min(mine.x, (int)a.vocab - 1), (int)min((unsigned)mine.y, (unsigned)a.n - 1));
+    mine = make_int2((int)min((unsigned)mine.x, (unsigned)a.vocab - 1), (int)min((unsigned)mine.y, (unsigned)a.n - 1));
     const int prev = lo > 0 ? __ldcg(&sorted[lo - 1].x) : -1;
     const int next = lo + m < count ? __ldcg(&sorted[lo + m].x) : -1;
     if (!a.accumulate && g < 32) {  // once, with the first span: a row's first token marks it
