@@ -660,6 +660,7 @@ cudaError_t norm(const NormArgs& a, cudaStream_t s) {
     }
 }
 
+// cols <= kNormCols: a wider row would take more warps than a block has.
 Shape grad_shape(int64_t rows, int64_t cols, int streams, int slot_bytes) {
     Shape f;
     // 2 granules a thread where they will do: with 3 or 4 the weight has to be
@@ -715,10 +716,14 @@ cudaError_t norm_grad(const NormGradArgs& a, int* parts, cudaStream_t s) {
     const bool aligned = a.cols % kGran == 0 && on_grid(a.grad, es) && on_grid(a.hidden, es) && on_grid(a.grad_hidden, es) &&
                          on_grid(a.grad_res, es) && on_grid(a.grad_x, es) && on_grid(Mat{const_cast<void*>(a.weight), 0}, es);
     const int mode = (a.grad_hidden.data ? kResidual : 0) | (a.mask.drops ? kDrops : 0);
-    const Shape f = grad_shape(a.rows, a.cols, a.grad_hidden.data ? 3 : 2, 16 * (aligned ? kSlot<true, T> : kSlot<false, T>));
-    // fp32 rows of more than about 8192 columns do not fit shared memory twice
-    if (a.cols > kNormCols || f.smem > kSmemMost || !fits_32(a.grad, es) || !fits_32(a.hidden, es) ||
-        !fits_32(a.grad_hidden, es) || !fits_32(a.grad_res, es) || !fits_32(a.grad_x, es)) {
+    bool wide = a.cols > kNormCols || !fits_32(a.grad, es) || !fits_32(a.hidden, es) || !fits_32(a.grad_hidden, es) ||
+                !fits_32(a.grad_res, es) || !fits_32(a.grad_x, es);
+    Shape f = {};
+    if (!wide) {
+        f = grad_shape(a.rows, a.cols, a.grad_hidden.data ? 3 : 2, 16 * (aligned ? kSlot<true, T> : kSlot<false, T>));
+        wide = f.smem > kSmemMost;  // fp32 rows of more than about 8192 columns do not fit shared memory twice
+    }
+    if (wide) {
         norm_grad_wide_kernel<T><<<(unsigned)a.rows, kWideThreads, 0, s>>>(a);
         count_launch();
         *parts = (int)(a.rows < kWideParts ? a.rows : kWideParts);
@@ -742,9 +747,11 @@ cudaError_t norm_grad(const NormGradArgs& a, int* parts, cudaStream_t s) {
 size_t norm_grad_bytes(int64_t rows, int64_t cols) {
     if (rows == 0 || cols == 0) return 0;
     // parts: a block's each, or the wide rows' shares
-    const int64_t grid = grad_shape(rows, cols, 2, 16).grid;
     int64_t parts = rows < kWideParts ? rows : kWideParts;
-    if (cols <= kNormCols && grid > parts) parts = grid;
+    if (cols <= kNormCols) {
+        const int64_t grid = grad_shape(rows, cols, 2, 16).grid;
+        if (grid > parts) parts = grid;
+    }
     return (size_t)parts * 2 * grad_stride(cols) * 4;
 }
 

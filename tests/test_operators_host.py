@@ -3,6 +3,9 @@ published answers, the mask's shape, and the refusals of the C ABI and of the
 binding, all of which come before anything is enqueued."""
 import ctypes
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -152,3 +155,16 @@ def test_binding_refuses_tensors_that_are_not_on_a_gpu():
         with pytest.raises(C.FsdpError) as e:
             call()
         assert e.value.code == C.FSDP_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("cols", [16384, 16385, 16640, 40000, 2 ** 34, 2 ** 40])
+def test_layer_norm_grad_workspace_of_wide_rows(cols):
+    # in a process of its own: an integer division by zero ends the process on some hosts
+    code = f"from hsdp_sharded_parameter_gb300 import capi as C; print(C.fsdp_layer_norm_grad_workspace(4, {cols}))"
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, (r.returncode, r.stderr)
+    assert int(r.stdout) == 4 * 2 * (-(-cols // 8) * 8) * 4  # a part a row, weight and bias
+    # the call asks the same question first
+    if cols <= 2 ** 34:
+        refused(norm_grad(cols=cols, gs=cols, hs=cols, xs=cols, wb=0), "workspace", "needs")
