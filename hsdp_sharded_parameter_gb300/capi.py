@@ -469,7 +469,7 @@ def fsdp_embedding(table, ids, out, scale=1.0, first_row=0, stream=None):
 
 
 def fsdp_embedding_grad_workspace(n_ids, vocab, cols):
-    """Bytes of the workspace that fsdp_embedding_grad needs."""
+    """Bytes of the workspace that fsdp_embedding_grad needs for n_ids tokens or fewer, into vocab rows or fewer."""
     b = ctypes.c_size_t()
     _check(lib().fsdp_embedding_grad_workspace(n_ids, vocab, cols, ctypes.byref(b)))
     return b.value
@@ -523,7 +523,7 @@ def fsdp_layer_norm(x, weight, bias, out, mean, rstd, eps=1e-5, residual=None, h
 
 
 def fsdp_layer_norm_grad_workspace(rows, cols):
-    """Bytes of the workspace that fsdp_layer_norm_grad needs."""
+    """Bytes of the workspace that fsdp_layer_norm_grad needs for that many rows or fewer."""
     b = ctypes.c_size_t()
     _check(lib().fsdp_layer_norm_grad_workspace(rows, cols, ctypes.byref(b)))
     return b.value

@@ -13,6 +13,8 @@
 //      marks the rows that a token names;
 //   3. the partial sums of the listed rows, added in order, and beside them
 //      the zeros of the rows that are not marked.
+#include <algorithm>
+
 #include "fsdp_ops.cuh"
 
 namespace fsdp {
@@ -147,9 +149,17 @@ int64_t up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
 // once (the fewer, the sooner the longest is done) and no long lists of parts
 // for rows of many tokens (57970 tokens, most in three rows of 16 columns: 84 us
 // with chunks of 8, 49 with 32), else 32.
-int chunk_tokens(int64_t n, int64_t cols) {
+struct ChunkRule {
+    int64_t most8, most16;  // tokens up to which a chunk has 8 and 16
+};
+ChunkRule chunk_rule(int64_t cols) {
     const int64_t spans = (cols + kSpan - 1) / kSpan, warps = 64 * (int64_t)sm_count();
-    return n <= 4096 && n * spans <= 8 * warps ? 8 : (n <= 16384 && n * spans <= 16 * warps ? 16 : 32);
+    if (spans == 0) return {4096, 16384};
+    return {std::min<int64_t>(4096, 8 * warps / spans), std::min<int64_t>(16384, 16 * warps / spans)};
+}
+int chunk_tokens(int64_t n, int64_t cols) {
+    const ChunkRule r = chunk_rule(cols);
+    return n <= r.most8 ? 8 : (n <= r.most16 ? 16 : 32);
 }
 
 GradWork grad_work(void* work, int64_t n, int64_t vocab, int64_t cols, size_t* bytes) {
@@ -854,6 +864,17 @@ size_t embedding_grad_bytes(int64_t n, int64_t vocab, int64_t cols) {
     size_t bytes = 0;
     grad_work(nullptr, n, vocab, cols, &bytes);
     return bytes;
+}
+
+// What any number of tokens up to n may need. While a chunk's tokens stay the
+// same, more tokens need more; where a chunk grows there are fewer parts, so
+// the last numbers of tokens before that count too.
+size_t embedding_grad_most_bytes(int64_t n, int64_t vocab, int64_t cols) {
+    const ChunkRule r = chunk_rule(cols);
+    size_t most = embedding_grad_bytes(n, vocab, cols);
+    for (const int64_t last : {r.most8, r.most16})
+        if (last < n) most = std::max(most, embedding_grad_bytes(last, vocab, cols));
+    return most;
 }
 
 cudaError_t launch_embedding(int table_dt, int out_dt, const EmbeddingArgs& a, cudaStream_t s) {

@@ -85,7 +85,9 @@ int sm_count();
 // device; `done` remembers the devices it was said for.
 cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done);
 
+// Workspace of a call, and one that serves every call of up to n tokens.
 size_t embedding_grad_bytes(int64_t n, int64_t vocab, int64_t cols);
+size_t embedding_grad_most_bytes(int64_t n, int64_t vocab, int64_t cols);
 size_t norm_grad_bytes(int64_t rows, int64_t cols);
 
 // Each enqueues its kernels (counting them) and returns the launches' error.

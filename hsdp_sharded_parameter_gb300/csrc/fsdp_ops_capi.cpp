@@ -156,7 +156,7 @@ int fsdp_embedding_grad_workspace(int64_t n_ids, int64_t vocab, int64_t cols, si
     if (!bytes) return bad(what, "bytes is NULL");
     FSDP_TRY(check_ids(what, FSDP_I64, n_ids > 0 ? &n_ids : nullptr, n_ids, vocab, cols));
     FSDP_TRY(check_size(what, n_ids, cols));
-    *bytes = embedding_grad_bytes(n_ids, vocab, cols);
+    *bytes = embedding_grad_most_bytes(n_ids, vocab, cols);
     return FSDP_OK;
 }
 

@@ -429,7 +429,8 @@ int fsdp_embedding(int table_dt, const void* table, int64_t table_stride, int64_
                    int index_type, const void* ids, int64_t n_ids, int64_t first_row, double scale,
                    int out_dt, void* out, int64_t out_stride, fsdp_stream_t stream);
 
-/* Scratch bytes of fsdp_embedding_grad. */
+/* Scratch bytes of fsdp_embedding_grad for n_ids tokens or any smaller number
+ * of them, into a table of vocab rows or fewer. */
 int fsdp_embedding_grad_workspace(int64_t n_ids, int64_t vocab, int64_t cols, size_t* bytes);
 
 /* Gradient of the lookup: grad_table[v] = scale * sum over t with
@@ -471,7 +472,7 @@ int fsdp_layer_norm(int64_t rows, int64_t cols, int dt, const void* x, int64_t x
                     int64_t hidden_stride, void* out, int64_t out_stride, float* mean, float* rstd,
                     fsdp_stream_t stream);
 
-/* Scratch bytes of fsdp_layer_norm_grad. */
+/* Scratch bytes of fsdp_layer_norm_grad for that many rows or fewer. */
 int fsdp_layer_norm_grad_workspace(int64_t rows, int64_t cols, size_t* bytes);
 
 /* Gradient of fsdp_layer_norm from hidden (its h; x where it had neither

@@ -171,6 +171,20 @@ def test_embedding_grad_of_many_tokens_is_exact_on_whole_numbers(n, vocab, kind)
     assert torch.equal(out.check().double(), want)
 
 
+@pytest.mark.parametrize("most, n", [(5000, 4096), (20000, 16384), (20000, 4096), (16385, 16384), (40000, 600)])
+def test_embedding_grad_of_fewer_tokens_than_the_workspace_was_sized_for(most, n):
+    vocab, cols = 300, 256
+    g = torch.Generator(device="cuda")
+    g.manual_seed(15)
+    grad = torch.randint(-8, 9, (n, cols), generator=g, device="cuda").float()
+    ids = ids_of(16, n, vocab, "hot")
+    out, work = Guarded(vocab, cols, F32), Workspace(C.fsdp_embedding_grad_workspace(most, vocab, cols))
+    C.fsdp_embedding_grad(grad, ids, out.t, work.t)
+    work.check()
+    want = torch.zeros(vocab, cols, dtype=torch.float64, device="cuda").index_add_(0, ids, grad.double())
+    assert torch.equal(out.check().double(), want)
+
+
 def test_embedding_grad_gives_equal_bits_and_keeps_other_rows_apart():
     n, vocab, cols = 30000, 500, 520
     grad, ids = rand(9, n, cols, BF16), ids_of(10, n, vocab, "hot")

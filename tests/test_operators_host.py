@@ -168,3 +168,16 @@ def test_layer_norm_grad_workspace_of_wide_rows(cols):
     # the call asks the same question first
     if cols <= 2 ** 34:
         refused(norm_grad(cols=cols, gs=cols, hs=cols, xs=cols, wb=0), "workspace", "needs")
+
+
+@pytest.mark.parametrize("cols", [8, 256, 5000, 40000])
+def test_a_workspace_serves_smaller_calls(cols):
+    # across every number of tokens at which the gradient's chunks grow, whatever the GPU
+    sizes = list(range(0, 600)) + list(range(600, 21000, 61)) + [4096, 4097, 16384, 16385, 65536, 10 ** 6]
+    got = [C.fsdp_embedding_grad_workspace(n, 32000, cols) for n in sorted(sizes)]
+    assert got == sorted(got)
+    for n in (1, 700, 20000):
+        got = [C.fsdp_embedding_grad_workspace(n, v, cols) for v in (0, 1, 31, 33, 4099, 32000, 131072)]
+        assert got == sorted(got)
+    got = [C.fsdp_layer_norm_grad_workspace(r, cols) for r in range(0, 6000)]
+    assert got == sorted(got)
