@@ -122,6 +122,7 @@ constexpr int kMaxBits = 9;      // of a digit: the counts of 32 warps take half
 constexpr int kSortCluster = 8;
 constexpr int kKeep = 8;         // tokens of a lane at a time
 constexpr int kTile = kSortThreads * kKeep;
+static_assert(kMaxGradTokens + 2 * kTile <= INT32_MAX, "a token's number and a tile fit an int");
 constexpr int kFewTokens = 512;  // summed without a sort
 
 // A row whose tokens lie in chunks first, first + 1, ..., first + more.

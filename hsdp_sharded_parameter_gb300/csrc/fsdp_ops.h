@@ -85,6 +85,9 @@ int sm_count();
 // device; `done` remembers the devices it was said for.
 cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done);
 
+// The gradient's sort numbers tokens in 32 bits and steps past the last one by
+// up to a tile.
+constexpr int64_t kMaxGradTokens = ((int64_t)1 << 31) - (1 << 14) - 1;
 // Workspace of a call, and one that serves every call of up to n tokens.
 size_t embedding_grad_bytes(int64_t n, int64_t vocab, int64_t cols);
 size_t embedding_grad_most_bytes(int64_t n, int64_t vocab, int64_t cols);

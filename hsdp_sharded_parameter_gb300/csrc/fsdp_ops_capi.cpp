@@ -75,10 +75,11 @@ int check_operands(const char* what, int64_t cols, std::initializer_list<Operand
     return FSDP_OK;
 }
 
-int check_ids(const char* what, int index_type, const void* ids, int64_t n, int64_t vocab, int64_t cols) {
+int check_ids(const char* what, int index_type, const void* ids, int64_t n, int64_t vocab, int64_t cols,
+              int64_t most = INT32_MAX - 1) {
     if (cols > INT32_MAX) return bad(what, "too many columns");
     if (index_type != FSDP_I32 && index_type != FSDP_I64) return bad(what, "unknown index type");
-    if (n < 0 || n >= INT32_MAX) return bad(what, "n_ids out of range");
+    if (n < 0 || n > most) return bad(what, "n_ids out of range");
     if (vocab < 0 || vocab >= INT32_MAX) return bad(what, "vocab out of range");
     if (n > 0 && !ids) return bad(what, "ids is NULL");
     if (reinterpret_cast<uintptr_t>(ids) % (index_type == FSDP_I64 ? 8 : 4)) return bad(what, "ids is not aligned to its element size");
@@ -154,7 +155,7 @@ int fsdp_embedding_grad_workspace(int64_t n_ids, int64_t vocab, int64_t cols, si
     const char* what = "embedding_grad_workspace";
     clear_error();
     if (!bytes) return bad(what, "bytes is NULL");
-    FSDP_TRY(check_ids(what, FSDP_I64, n_ids > 0 ? &n_ids : nullptr, n_ids, vocab, cols));
+    FSDP_TRY(check_ids(what, FSDP_I64, n_ids > 0 ? &n_ids : nullptr, n_ids, vocab, cols, kMaxGradTokens));
     FSDP_TRY(check_size(what, n_ids, cols));
     *bytes = embedding_grad_most_bytes(n_ids, vocab, cols);
     return FSDP_OK;
@@ -166,7 +167,7 @@ int fsdp_embedding_grad(int grad_dt, const void* grad_out, int64_t grad_out_stri
                         size_t workspace_bytes, fsdp_stream_t stream) {
     const char* what = "embedding_grad";
     clear_error();
-    FSDP_TRY(check_ids(what, index_type, ids, n_ids, vocab, cols));
+    FSDP_TRY(check_ids(what, index_type, ids, n_ids, vocab, cols, kMaxGradTokens));
     FSDP_TRY(check_size(what, n_ids, cols));
     FSDP_TRY(check_operands(what, cols, {{"grad_out", grad_out, grad_out_stride, grad_dt, n_ids, false, false},
                                          {"grad_table", grad_table, grad_table_stride, table_dt, vocab, true, false}}));

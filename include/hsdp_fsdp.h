@@ -424,7 +424,8 @@ enum fsdp_index_type { FSDP_I32 = 0, FSDP_I64 = 1 };
  * cast to out_dt. An id outside [first_row, first_row + vocab) names no row
  * and gives a row of zeros: padding tokens (-1, say), or, with first_row set
  * on a table that holds a slice of the vocabulary, tokens of other slices.
- * vocab, n_ids < 2^31 - 1, cols < 2^31, here and in the gradient. */
+ * vocab, n_ids < 2^31 - 1, cols < 2^31, here and in the gradient, where
+ * n_ids < 2^31 - 2^14. */
 int fsdp_embedding(int table_dt, const void* table, int64_t table_stride, int64_t vocab, int64_t cols,
                    int index_type, const void* ids, int64_t n_ids, int64_t first_row, double scale,
                    int out_dt, void* out, int64_t out_stride, fsdp_stream_t stream);

@@ -181,3 +181,17 @@ def test_a_workspace_serves_smaller_calls(cols):
         assert got == sorted(got)
     got = [C.fsdp_layer_norm_grad_workspace(r, cols) for r in range(0, 6000)]
     assert got == sorted(got)
+
+
+@pytest.mark.parametrize("n", [2 ** 31 - 2 ** 14, 2 ** 31 - 8192, 2 ** 31 - 2])
+def test_embedding_grad_refuses_tokens_that_its_sort_cannot_number(n):
+    # a step of 8192 tokens past the last one, and the next, have to fit 32 bits with a sign
+    refused(emb_grad(n=n, wb=2 ** 62), "n_ids")
+    b = ctypes.c_size_t()
+    refused(C.lib().fsdp_embedding_grad_workspace(n, 4, 8, ctypes.byref(b)), "n_ids")
+
+
+def test_embedding_grad_takes_as_many_tokens_as_the_header_says():
+    n = 2 ** 31 - 2 ** 14 - 1
+    assert C.fsdp_embedding_grad_workspace(n, 4, 8) > 16 * n  # two buffers of (row, token)
+    refused(emb_grad(n=n, wb=16 * n), "workspace", "needs")
