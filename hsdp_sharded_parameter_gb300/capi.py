@@ -370,14 +370,18 @@ _TYPES = {}
 
 
 def _types():
-    """torch dtypes of the operators' values and of their ids, as the C ABI's."""
+    """torch dtypes of the operators' values and of their ids, as the C ABI's.
+    The table appears whole: other threads may be at their first call too."""
+    global _TYPES
     import torch
 
-    _TYPES["ids"] = {torch.int32: FSDP_I32, torch.int64: FSDP_I64}
-    _TYPES["device"] = torch.cuda.current_device
-    # the current stream's handle without a Stream object around it (2.8 us a call)
-    _TYPES["stream"] = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-    _TYPES.update({torch.float32: FSDP_F32, torch.bfloat16: FSDP_BF16})
+    _TYPES = {
+        torch.float32: FSDP_F32, torch.bfloat16: FSDP_BF16,
+        "ids": {torch.int32: FSDP_I32, torch.int64: FSDP_I64},
+        "device": torch.cuda.current_device,
+        # the current stream's handle without a Stream object around it (2.8 us a call)
+        "stream": getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream),
+    }
     return _TYPES
 
 

@@ -6,6 +6,7 @@ import math
 import os
 import subprocess
 import sys
+import threading
 
 import numpy as np
 import pytest
@@ -195,3 +196,41 @@ def test_embedding_grad_takes_as_many_tokens_as_the_header_says():
     n = 2 ** 31 - 2 ** 14 - 1
     assert C.fsdp_embedding_grad_workspace(n, 4, 8) > 16 * n  # two buffers of (row, token)
     refused(emb_grad(n=n, wb=16 * n), "workspace", "needs")
+
+
+class OnGpu:
+    """What the binding asks of a 4 x 8 float32 tensor on the first GPU."""
+    dtype, is_cuda, shape, device = torch.float32, True, (4, 8), "cuda:0"
+    stride, data_ptr, get_device = (lambda self: (8, 1)), (lambda self: P), (lambda self: 0)
+
+
+def test_first_calls_from_several_threads(monkeypatch):
+    # a second thread's first call, made between any two lines of the first
+    # thread's as soon as there is something in the table
+    monkeypatch.setattr(C, "_TYPES", {})
+    want, seen = (P, 4, 8, 8, C.FSDP_F32, 0), []
+
+    def second():
+        sys.settrace(None)  # of this thread
+        try:
+            seen.append(C._matrix("test", "x", OnGpu()))
+        except Exception as e:
+            seen.append(e)
+
+    def trace(frame, event, arg):
+        if frame.f_code is not C._types.__code__:
+            return None
+        if not C._TYPES:
+            return trace
+        t = threading.Thread(target=second)
+        t.start()
+        t.join(30)
+        return trace
+
+    old = sys.gettrace()
+    sys.settrace(trace)
+    try:
+        got = C._matrix("test", "x", OnGpu())
+    finally:
+        sys.settrace(old)
+    assert got == want and seen and all(s == want for s in seen), seen
