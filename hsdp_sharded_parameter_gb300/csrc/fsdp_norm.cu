@@ -180,7 +180,10 @@ __global__ void __launch_bounds__(V == 2 ? 256 : (V == 1 ? 128 : 512), V == 2 ? 
         }
         float sum[1] = {s.x + s.y};
         group_sum(sum, gw, group, warp, lane, 0);
-        const float mean = sum[0] / (float)cols;  // equal values give their own; a product with 1 / cols may not
+        // one rounding: where the sum of equal values is exact (few bits, or few
+        // columns) they give their own, which a product with 1 / cols may not;
+        // else their mean is off by the sum's roundings
+        const float mean = sum[0] / (float)cols;
         s = both(0.0f);
 #pragma unroll
         for (int v = 0; v < V; ++v) {

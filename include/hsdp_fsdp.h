@@ -466,7 +466,9 @@ int fsdp_dropout(int64_t rows, int64_t cols, int dt, const void* x, int64_t x_st
  * mean = sum h / cols, rstd = 1 / sqrt(sum (h - mean)^2 / cols + eps), from h
  * before any rounding. weight (NULL: 1) and bias (NULL: 0) hold cols elements
  * of param_dt. hidden, when not NULL, receives h; mean and rstd, when not
- * NULL, rows values each. All matrices have dtype dt. */
+ * NULL, rows values each. All matrices have dtype dt. eps >= 0. The sums are
+ * binary32's: the mean of a row of equal values may differ from them by the
+ * sum's roundings, and with eps = 0 the output of such a row is not defined. */
 int fsdp_layer_norm(int64_t rows, int64_t cols, int dt, const void* x, int64_t x_stride,
                     const void* residual, int64_t residual_stride, double p, uint64_t seed, uint32_t draw,
                     int param_dt, const void* weight, const void* bias, double eps, void* hidden,

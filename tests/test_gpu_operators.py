@@ -376,6 +376,20 @@ def test_layer_norm_of_constant_and_loud_rows():
     R.agree("rstd", rstd.t[0, keep], want["rstd"])
 
 
+@pytest.mark.parametrize("cols", [1000, 1001, 8192, 20000])
+def test_layer_norm_of_constant_rows_of_many_bits(cols):
+    # sums of equal values that are not exact: mean and output within binary32's bounds, not equal to the value and the bias
+    values = torch.tensor([0.64042264, -0.5356694, 0.1, 1.0 / 3.0, -7.0, 0.0], device="cuda")
+    x = values[:, None].expand(-1, cols).contiguous()
+    w, b = vec(3, cols, F32, 1.0), vec(4, cols, F32)
+    out, mean, rstd = Guarded(len(values), cols, F32), Guarded(1, len(values), F32), Guarded(1, len(values), F32)
+    C.fsdp_layer_norm(x, w, b, out.t, mean.t, rstd.t)
+    want = R.layer_norm(x, w, b, 1e-5)
+    for name, got in (("out", out), ("mean", mean), ("rstd", rstd)):
+        R.agree(name, got.check(), want[name])
+    assert torch.equal(out.t[4:], b.expand(2, cols)) and torch.equal(mean.t[0, 4:], values[4:])  # exact sums
+
+
 @pytest.mark.parametrize("dt, pdt", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32"), ("f32", "bf16")])
 @pytest.mark.parametrize("rows, cols, pad, offset", NORM_SIZES)
 def test_layer_norm_grad(dt, pdt, rows, cols, pad, offset):
