@@ -234,3 +234,24 @@ def test_first_calls_from_several_threads(monkeypatch):
     finally:
         sys.settrace(old)
     assert got == want and seen and all(s == want for s in seen), seen
+
+
+@pytest.mark.parametrize("change, word", [(dict(draw=2 ** 32), "draw"), (dict(draw=-(2 ** 31) - 1), "draw"), (dict(seed=2 ** 64), "seed"),
+                                          (dict(seed=-(2 ** 63) - 1), "seed")])
+def test_binding_refuses_numbers_that_a_mask_would_cut(change, word):
+    # 2^32 would draw the mask of 0 again
+    x, a = torch.zeros(4, 8), dict(p=0.5, seed=1, draw=0)
+    a.update(change)
+    for call in [lambda: C.fsdp_dropout(x, x, **a), lambda: C.fsdp_layer_norm(x, None, None, x, None, None, **a),
+                 lambda: C.fsdp_layer_norm_grad(x, x, x, x, None, x, None, None, x, **a)]:
+        with pytest.raises(C.FsdpError, match=word) as e:
+            call()
+        assert e.value.code == C.FSDP_ERR_INVALID_ARG
+
+
+def test_binding_refuses_a_first_row_that_would_be_cut():
+    x, ids = torch.zeros(4, 8), torch.zeros(4, dtype=torch.int64)
+    for first in (2 ** 63, 2 ** 64 + 5, -(2 ** 63) - 1):
+        for call in [lambda: C.fsdp_embedding(x, ids, x, first_row=first), lambda: C.fsdp_embedding_grad(x, ids, x, x, first_row=first)]:
+            with pytest.raises(C.FsdpError, match="first_row"):
+                call()
