@@ -12,16 +12,6 @@ namespace {
 // A lane holds granules of 8 consecutive columns, a warp a span of 256.
 constexpr int kSpan = 32 * kGran;
 
-// The types as the kernels hold them.
-template <int DT>
-struct ElemOf {
-    using type = float;
-};
-template <>
-struct ElemOf<FSDP_BF16> {
-    using type = uint16_t;
-};
-
 // Bytes [sh, sh + 16) of the 32-byte string lo:hi, sh below 16 and a multiple
 // of T's size: two rounds of selections by sh's bits, and for 16-bit elements
 // a shift.
