@@ -703,9 +703,14 @@ cudaError_t grad_rows(const NormGradArgs& a, const Shape& f, int64_t stride, cud
 }
 template <typename T, bool kAligned, int kMode>
 cudaError_t grad_v(const NormGradArgs& a, const Shape& f, int64_t stride, cudaStream_t s) {
+    if constexpr (sizeof(T) == 2) {
+        if (f.v == 4) return grad_rows<T, 4, kAligned, kMode>(a, f, stride, s);
+    } else {
+        // rows of 4 granules a thread, 13 warps and more, are among the wide ones
+        static_assert((int64_t)13 * 4 * 16 * kSlot<true, T> * 2 * 2 > kSmemMost, "two rows do not fit");
+    }
     return f.v == 1 ? grad_rows<T, 1, kAligned, kMode>(a, f, stride, s)
-           : f.v == 2 ? grad_rows<T, 2, kAligned, kMode>(a, f, stride, s)
-           : f.v == 3 ? grad_rows<T, 3, kAligned, kMode>(a, f, stride, s) : grad_rows<T, 4, kAligned, kMode>(a, f, stride, s);
+           : f.v == 2 ? grad_rows<T, 2, kAligned, kMode>(a, f, stride, s) : grad_rows<T, 3, kAligned, kMode>(a, f, stride, s);
 }
 
 constexpr int kWideParts = 256;
