@@ -96,6 +96,21 @@ def test_embedding(tdt, odt, n, vocab, cols, pad, offset):
     R.agree("out", out.check(), R.embedding(table, ids, math.sqrt(cols), 0, NAMES[odt]))
 
 
+# more than one block of the narrow kernel (1024 granules), on the grid and off it, and of the wide one, in one and in several steps a row
+MANY_TOKENS = [(1500, 300, 8, 0, 0), (1030, 77, 40, 0, 0), (700, 50, 93, 0, 1), (700, 50, 200, 0, 0), (500, 40, 201, 3, 0), (300, 90, 520, 0, 0),
+               (150, 33, 1111, 0, 3), (70, 20, 4104, 0, 0), (65, 20, 4999, 1, 0)]
+
+
+@pytest.mark.parametrize("tdt, odt", list(itertools.product(NAMES, NAMES)))
+@pytest.mark.parametrize("n, vocab, cols, pad, offset", MANY_TOKENS)
+def test_embedding_of_many_tokens(tdt, odt, n, vocab, cols, pad, offset):
+    table = rand(1, vocab, cols, NAMES[tdt], 0.02, pad, offset)
+    ids = ids_of(2, n, vocab, "wild", torch.int32 if n % 2 else torch.int64)
+    out = Guarded(n, cols, NAMES[odt], pad, (offset * 3) % 8)
+    C.fsdp_embedding(table, ids, out.t, scale=0.7)
+    R.agree("out", out.check(), R.embedding(table, ids, 0.7, 0, NAMES[odt]))
+
+
 def test_embedding_ids_beyond_32_bits_and_a_slice_of_the_vocabulary():
     table = rand(1, 10, 40, BF16)
     ids = torch.tensor([2 ** 32 + 3, 2 ** 40, -(2 ** 63), 2 ** 63 - 1, 100, 109, 110, 99, 3], device="cuda")
