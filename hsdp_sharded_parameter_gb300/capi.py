@@ -458,18 +458,19 @@ def _work(what, t, dev):
     return t.data_ptr(), t.numel() * t.element_size()
 
 
-def _mask(what, seed, draw):
-    """A mask's numbers have to fit the C ABI's types, which would cut them and
-    draw the mask of others again. (Negative ones stand for their bits.)"""
-    if not -(1 << 31) <= draw < 1 << 32:
-        _refuse(what, f"draw {draw} does not fit 32 bits")
-    if not -(1 << 63) <= seed < 1 << 64:
-        _refuse(what, f"seed {seed} does not fit 64 bits")
+# Numbers that do not fit the C ABI's types would be cut: another first row, or
+# the mask of another draw again. (Negative draws and seeds stand for their
+# bits.) Compared in the calls themselves, which a function would cost 0.1 us.
+_I32, _I64 = -(1 << 31), -(1 << 63)
+_U32, _U64, _TOP64 = (1 << 32) - 1, (1 << 64) - 1, (1 << 63) - 1
 
 
-def _first(what, first_row):
-    if not -(1 << 63) <= first_row < 1 << 63:
-        _refuse(what, f"first_row {first_row} does not fit 64 bits")
+def _no_mask(what, seed, draw):
+    _refuse(what, f"seed {seed} does not fit 64 bits" if _I32 <= draw <= _U32 else f"draw {draw} does not fit 32 bits")
+
+
+def _no_row(what, first_row):
+    _refuse(what, f"first_row {first_row} does not fit 64 bits")
 
 
 def fsdp_embedding(table, ids, out, scale=1.0, first_row=0, stream=None):
@@ -477,7 +478,8 @@ def fsdp_embedding(table, ids, out, scale=1.0, first_row=0, stream=None):
     row of the table. table: (vocab, cols); ids: n int32 or int64; out:
     (n, cols), float32 or bfloat16 whatever the table's type."""
     what = "embedding"
-    _first(what, first_row)
+    if not _I64 <= first_row <= _TOP64:
+        _no_row(what, first_row)
     tp, vocab, cols, ts, tdt, dev = _matrix(what, "table", table)
     it, ip, n = _ids(what, ids, dev)
     op, rows, ocols, os_, odt, odev = _matrix(what, "out", out)
@@ -500,7 +502,8 @@ def fsdp_embedding_grad(grad_out, ids, grad_table, workspace, scale=1.0, first_r
     added to what grad_table holds. workspace: a tensor of at least
     fsdp_embedding_grad_workspace(n, vocab, cols) bytes."""
     what = "embedding_grad"
-    _first(what, first_row)
+    if not _I64 <= first_row <= _TOP64:
+        _no_row(what, first_row)
     gp, rows, cols, gs, gdt, dev = _matrix(what, "grad_out", grad_out)
     it, ip, n = _ids(what, ids, dev)
     tp, vocab, tcols, ts, tdt, tdev = _matrix(what, "grad_table", grad_table)
@@ -518,7 +521,8 @@ def fsdp_dropout(x, out, p, seed, draw=0, residual=None, stream=None):
     backward pass is this call on the gradient. out may be x or residual. seed
     has 64 bits, draw 32."""
     what = "dropout"
-    _mask(what, seed, draw)
+    if not (_I32 <= draw <= _U32 and _I64 <= seed <= _U64):
+        _no_mask(what, seed, draw)
     xp, rows, cols, xs, dt, dev = _matrix(what, "x", x)
     rp, rs = _like(what, "residual", residual, rows, cols, dt, dev)
     op, os_ = _like(what, "out", out, rows, cols, dt, dev)
@@ -532,7 +536,8 @@ def fsdp_layer_norm(x, weight, bias, out, mean, rstd, eps=1e-5, residual=None, h
     p = 0: of x), times weight plus bias (either may be None). hidden receives
     h, mean and rstd (float32) each row's; any of the three may be None."""
     what = "layer_norm"
-    _mask(what, seed, draw)
+    if not (_I32 <= draw <= _U32 and _I64 <= seed <= _U64):
+        _no_mask(what, seed, draw)
     xp, rows, cols, xs, dt, dev = _matrix(what, "x", x)
     rp, rs = _like(what, "residual", residual, rows, cols, dt, dev)
     hp, hs = _like(what, "hidden", hidden, rows, cols, dt, dev)
@@ -561,7 +566,8 @@ def fsdp_layer_norm_grad(grad_out, hidden, mean, rstd, weight, grad_x, grad_weig
     gradient that reaches hidden past the norm. workspace: a tensor of at least
     fsdp_layer_norm_grad_workspace(rows, cols) bytes."""
     what = "layer_norm_grad"
-    _mask(what, seed, draw)
+    if not (_I32 <= draw <= _U32 and _I64 <= seed <= _U64):
+        _no_mask(what, seed, draw)
     gp, rows, cols, gs, dt, dev = _matrix(what, "grad_out", grad_out)
     hp, hs = _like(what, "hidden", hidden, rows, cols, dt, dev)
     ap, as_ = _like(what, "grad_hidden", grad_hidden, rows, cols, dt, dev)
