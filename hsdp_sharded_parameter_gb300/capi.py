@@ -498,9 +498,9 @@ def fsdp_embedding_grad_workspace(n_ids, vocab, cols):
 
 def fsdp_embedding_grad(grad_out, ids, grad_table, workspace, scale=1.0, first_row=0, accumulate=False, stream=None):
     """grad_table[v] = scale * sum of grad_out[t] over the tokens t that name
-    row v, in ascending order of t; zeros where there is none. With accumulate,
-    added to what grad_table holds. workspace: a tensor of at least
-    fsdp_embedding_grad_workspace(n, vocab, cols) bytes."""
+    row v, in an order that is the same for equal calls; zeros where there is
+    none. With accumulate, added to what grad_table holds. workspace: a tensor
+    of at least fsdp_embedding_grad_workspace(n, vocab, cols) bytes."""
     what = "embedding_grad"
     if not _I64 <= first_row <= _TOP64:
         _no_row(what, first_row)

@@ -148,8 +148,8 @@ int64_t up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
 
 // Tokens of a chunk: few while that gives no more warps than the GPU holds at
 // once (the fewer, the sooner the longest is done) and no long lists of parts
-// for rows of many tokens (57970 tokens, most in three rows of 16 columns: 84 us
-// with chunks of 8, 49 with 32), else 32.
+// for rows of many tokens (57970 tokens, most in three rows of 16 columns: 42 us
+// with chunks of 8, 37 with 32), else 32.
 struct ChunkRule {
     int64_t most8, most16;  // tokens up to which a chunk has 8 and 16
 };
@@ -775,10 +775,10 @@ cudaError_t embedding_grad_few(const EmbeddingGradArgs& a, cudaStream_t s) {
 
 template <typename S, typename D, bool kAligned>
 cudaError_t embedding_grad_as(const EmbeddingGradArgs& a, cudaStream_t s) {
-    // One kernel against three: 64 tokens into 32000 x 4096 bf16 38 and 49 us,
-    // 300 into 4099 x 1027 fp32, nine in ten of them in three rows, 12 and 20,
-    // spread 9 and 21. With many tokens a row it falls behind, a block having
-    // a row's tokens to itself: 512 into 7 rows of 8192 45 and 16.
+    // One kernel against three, calls in a row: 64 tokens into 32000 x 4096 bf16
+    // 41 and 53 us, 300 into 4099 x 1027 fp32, nine in ten of them in three
+    // rows, 14 and 23, spread 10 and 23. With many tokens a row it falls behind,
+    // a block having a row's tokens to itself: 512 into 7 rows of 8192 45 and 20.
     if (a.n <= kFewTokens && a.n <= 8 * a.vocab && a.cols <= (int64_t)65535 * kGroup * kSpan)
         return embedding_grad_few<S, D, kAligned>(a, s);
     const GradWork w = grad_work(a.work, a.n, a.vocab, a.cols, nullptr);

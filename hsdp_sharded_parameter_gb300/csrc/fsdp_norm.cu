@@ -604,8 +604,8 @@ Shape norm_shape(int64_t rows, int64_t cols, int streams, int slot_bytes) {
     Shape f;
     const int64_t grans = (cols + kGran - 1) / kGran;
     // few warps a row make its two sums cheap: 16384 rows of bf16 with dropout
-    // and residual take 29 us at 1024 columns with 2 granules a thread and 32
-    // with 1, 88 at 4096 with 4 and 111 with 2, 167 at 8192 with 4 and 219
+    // and residual take 31 us at 1024 columns with 2 granules a thread and 34
+    // with 1, 91 at 4096 with 4 and 114 with 2, 166 at 8192 with 4 and 219
     // with 2. Rows that do not fill the GPU are done sooner by more warps (16
     // of 4096 columns: 3.4 us with 2 granules, 4.2 with 4).
     const int spans = (int)((cols + kSpan - 1) / kSpan);

@@ -414,8 +414,8 @@ int fsdp_rs_ar_reduce_noalloc(fsdp_plan_t plan, int grad_dtype, const void* cons
  *
  * Numerics: everything between an operator's inputs and outputs is computed
  * and summed in binary32 and rounded once to the output's type. Sums are
- * taken in an order fixed by the sizes and the GPU's number of SMs, so equal
- * calls give equal bits. A
+ * taken in an order fixed by the sizes, types, strides and alignments of the
+ * operands and the GPU's number of SMs, so equal calls give equal bits. A
  * result that is not a number is some NaN. */
 
 enum fsdp_index_type { FSDP_I32 = 0, FSDP_I64 = 1 };
@@ -435,9 +435,11 @@ int fsdp_embedding(int table_dt, const void* table, int64_t table_stride, int64_
 int fsdp_embedding_grad_workspace(int64_t n_ids, int64_t vocab, int64_t cols, size_t* bytes);
 
 /* Gradient of the lookup: grad_table[v] = scale * sum over t with
- * ids[t] - first_row = v of grad_out[t], the tokens of a row taken in
- * ascending order after a stable sort; rows that no token names become zero,
- * and tokens that name no row are left out. With accumulate != 0 the result
+ * ids[t] - first_row = v of grad_out[t]; rows that no token names become
+ * zero, and tokens that name no row are left out. A row's tokens are sorted
+ * and cut into parts, each summed in ascending order of t, and the parts' sums
+ * are added, some of them side by side: an order that is the same every time,
+ * but not that of t throughout. With accumulate != 0 the result
  * is added, in binary32, to what grad_table holds and rounded once, and rows
  * that no token names are not touched (gradient accumulation; an embedding
  * tied to an output projection). */
