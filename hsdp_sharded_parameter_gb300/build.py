@@ -4,7 +4,8 @@ The translation units are compiled in parallel and linked with nvcc:
   * csrc/fsdp_kernels.cu -- the sm_103a kernels (nvcc, one -gencode)
   * csrc/fsdp_bulk.cu    -- the bulk-fed fused reduce of a capped grid
   * csrc/fsdp_noalloc.cu -- the allocation-free fused gradient sync
-  * csrc/fsdp_embedding.cu, fsdp_dropout.cu, fsdp_norm.cu -- the training operators
+  * csrc/fsdp_embedding.cu, fsdp_dropout.cu, fsdp_norm.cu, fsdp_ffn.cu, fsdp_ortho.cu -- the
+    training operators
   * csrc/fsdp_capi.cpp   -- plan, bindings and entry points (host C++)
   * csrc/fsdp_ops_capi.cpp -- entry points of the training operators (host C++)
 No fast-math, no FMA contraction, no flush-to-zero: the kernels' additions,
@@ -27,7 +28,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-Wall", "-ftz=false",
               "-prec-div=true", "-prec-sqrt=true", "-fmad=false", "--expt-relaxed-constexpr"]
 CUDA_SOURCES = ["fsdp_kernels.cu", "fsdp_noalloc.cu", "fsdp_bulk.cu", "fsdp_embedding.cu", "fsdp_dropout.cu",
-                "fsdp_norm.cu"]
+                "fsdp_norm.cu", "fsdp_ffn.cu", "fsdp_ortho.cu"]
 CXX_SOURCES = ["fsdp_capi.cpp", "fsdp_ops_capi.cpp"]
 CXX_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra"]
 

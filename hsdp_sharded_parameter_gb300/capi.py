@@ -21,6 +21,7 @@ FSDP_OK, FSDP_ERR_INVALID_ARG, FSDP_ERR_NOT_IMPLEMENTED, FSDP_ERR_CUDA, FSDP_ERR
 FSDP_F32, FSDP_BF16 = 0, 1
 FSDP_AVG, FSDP_SUM = 0, 1
 FSDP_I32, FSDP_I64 = 0, 1
+FSDP_SILU, FSDP_GELU, FSDP_RELU = 0, 1, 2
 FSDP_STATUS_PRODUCER_WAIT, FSDP_STATUS_CONSUMER_WAIT, FSDP_STATUS_ORDER = 1, 2, 4
 (FSDP_ROLE_SHARDS, FSDP_ROLE_AG_OUTPUT, FSDP_ROLE_FULL_PARAMS, FSDP_ROLE_GRADS,
  FSDP_ROLE_RS_INPUT, FSDP_ROLE_FUSED, FSDP_ROLE_SHARD_GRADS) = range(7)
@@ -33,6 +34,7 @@ DTYPES = {"f32": FSDP_F32, "bf16": FSDP_BF16}
 # roles that take one buffer per (rank, parameter); the others one per rank
 PER_PARAM_ROLES = {FSDP_ROLE_SHARDS, FSDP_ROLE_FULL_PARAMS, FSDP_ROLE_GRADS, FSDP_ROLE_SHARD_GRADS}
 OPS = {"avg": FSDP_AVG, "sum": FSDP_SUM}
+ACTIVATIONS = {"silu": FSDP_SILU, "gelu": FSDP_GELU, "relu": FSDP_RELU}
 
 _lib = None
 
@@ -104,6 +106,15 @@ def lib():
         L.fsdp_layer_norm_grad_workspace.argtypes = [i64, i64, P(sz)]
         L.fsdp_layer_norm_grad.argtypes = [i64, i64, i32, vp, i64, vp, i64, vp, i64, vp, vp, i32, vp, f64, u64, u32,
                                            i32, vp, i64, vp, i64, i32, vp, vp, vp, sz, vp]
+        L.fsdp_operators_status.argtypes = [vp, P(i32)]
+        L.fsdp_gated_ffn_workspace.argtypes = [i64, i64, i64, i32, P(sz)]
+        L.fsdp_gated_ffn.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, i32, vp, i64, vp, i64, vp, i64,
+                                     vp, sz, vp]
+        L.fsdp_gated_ffn_grad_workspace.argtypes = [i64, i64, i64, i32, P(sz)]
+        L.fsdp_gated_ffn_grad.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64,
+                                          i32, vp, i64, i32, i32, vp, i64, vp, i64, vp, i64, vp, sz, vp]
+        L.fsdp_orthogonalize_workspace.argtypes = [i64, i64, P(sz)]
+        L.fsdp_orthogonalize.argtypes = [i64, i64, i32, vp, i64, i32, f64, f64, f64, f64, f64, vp, i64, vp, sz, vp]
         _lib = L
     return _lib
 
@@ -582,3 +593,121 @@ def fsdp_layer_norm_grad(grad_out, hidden, mean, rstd, weight, grad_x, grad_weig
     _check(lib().fsdp_layer_norm_grad(rows, cols, dt, gp, gs, ap, as_, hp, hs, mp, sp, FSDP_F32 if wdt is None else wdt,
                                       wp, p, seed, draw, int(accumulate), rp, rs, xp, xs, gdt, dwp, dbp, kp, kb,
                                       handle))
+
+
+# ----------------------------------------- products of a feed-forward block
+#
+# Matrices are passed as above, in bfloat16 where nothing else is said.
+
+
+def fsdp_operators_status(stream=None):
+    """1 when a wait inside a kernel of the operators below has run out since
+    the last question (their results are then undefined), else 0. Synchronises
+    the stream."""
+    v = ctypes.c_int(0)
+    _check(lib().fsdp_operators_status(_stream(stream), ctypes.byref(v)))
+    return v.value
+
+
+def _aligned(hidden, inner, aligned):
+    return int(hidden % 8 == 0 and inner % 8 == 0) if aligned is None else int(bool(aligned))
+
+
+def fsdp_gated_ffn_workspace(tokens, hidden, inner, aligned=None):
+    """Bytes of the workspace that fsdp_gated_ffn needs for that many tokens or
+    fewer. aligned: whether the rows of all its matrices start on the 16-byte
+    grid, as contiguous ones do where hidden and inner are multiples of 8 (the
+    default: whether they are)."""
+    b = ctypes.c_size_t()
+    _check(lib().fsdp_gated_ffn_workspace(tokens, hidden, inner, _aligned(hidden, inner, aligned), ctypes.byref(b)))
+    return b.value
+
+
+def _activation(what, name):
+    act = ACTIVATIONS.get(name, name)
+    if not isinstance(act, int):
+        _refuse(what, f"activation {name!r} is none of {sorted(ACTIVATIONS)}")
+    return act
+
+
+def fsdp_gated_ffn(x, w_gate, w_up, w_down, out, workspace, activation="silu", gate=None, up=None, stream=None):
+    """out = (act(x w_gate^T) * (x w_up^T)) w_down^T. x, out: (tokens, hidden);
+    w_gate, w_up: (inner, hidden); w_down: (hidden, inner); gate and up, both or
+    neither given, receive the two projections (tokens, inner), which the
+    gradient needs. activation: "silu", "gelu" or "relu". workspace: a tensor of
+    at least fsdp_gated_ffn_workspace(tokens, hidden, inner) bytes."""
+    what = "gated_ffn"
+    xp, rows, cols, xs, dt, dev = _matrix(what, "x", x)
+    if dt != FSDP_BF16:
+        _refuse(what, f"x is {x.dtype}; expected bfloat16")
+    gp, inner, gcols, gs, _, _ = _matrix(what, "w_gate", w_gate)
+    _like(what, "w_gate", w_gate, inner, cols, dt, dev)
+    up_, us = _like(what, "w_up", w_up, inner, cols, dt, dev)
+    dp, ds = _like(what, "w_down", w_down, cols, inner, dt, dev)
+    kg, kgs = _like(what, "gate", gate, rows, inner, dt, dev)
+    ku, kus = _like(what, "up", up, rows, inner, dt, dev)
+    if (gate is None) != (up is None):
+        _refuse(what, "gate and up: one of them is None")
+    op, os_ = _like(what, "out", out, rows, cols, dt, dev)
+    act = _activation(what, activation)
+    wp, wb = _work(what, workspace, dev)
+    handle = _on(what, dev, stream)
+    _check(lib().fsdp_gated_ffn(rows, cols, inner, xp, xs, gp, gs, up_, us, dp, ds, act, kg, kgs, ku, kus, op, os_, wp, wb,
+                                handle))
+
+
+def fsdp_gated_ffn_grad_workspace(tokens, hidden, inner, aligned=None):
+    """Bytes of the workspace that fsdp_gated_ffn_grad needs, as fsdp_gated_ffn_workspace."""
+    b = ctypes.c_size_t()
+    _check(lib().fsdp_gated_ffn_grad_workspace(tokens, hidden, inner, _aligned(hidden, inner, aligned), ctypes.byref(b)))
+    return b.value
+
+
+def fsdp_gated_ffn_grad(grad_out, x, w_gate, w_up, w_down, gate, up, grad_x, grad_w_gate, grad_w_up, grad_w_down, workspace,
+                        activation="silu", accumulate=False, stream=None):
+    """Gradient of fsdp_gated_ffn from the gate and up that it gave: grad_x and
+    the three weights' gradients, float32 or bfloat16 (with accumulate, added to
+    what they hold). workspace: a tensor of at least
+    fsdp_gated_ffn_grad_workspace(tokens, hidden, inner) bytes."""
+    what = "gated_ffn_grad"
+    gp, rows, cols, gs, dt, dev = _matrix(what, "grad_out", grad_out)
+    if dt != FSDP_BF16:
+        _refuse(what, f"grad_out is {grad_out.dtype}; expected bfloat16")
+    xp, xs = _like(what, "x", x, rows, cols, dt, dev)
+    wgp, inner, _, wgs, _, _ = _matrix(what, "w_gate", w_gate)
+    _like(what, "w_gate", w_gate, inner, cols, dt, dev)
+    wup, wus = _like(what, "w_up", w_up, inner, cols, dt, dev)
+    wdp, wds = _like(what, "w_down", w_down, cols, inner, dt, dev)
+    kg, kgs = _like(what, "gate", gate, rows, inner, dt, dev)
+    ku, kus = _like(what, "up", up, rows, inner, dt, dev)
+    dxp, dxs = _like(what, "grad_x", grad_x, rows, cols, dt, dev)
+    pdt = (_TYPES or _types()).get(grad_w_gate.dtype)
+    dgp, dgs = _like(what, "grad_w_gate", grad_w_gate, inner, cols, pdt, dev)
+    dup, dus = _like(what, "grad_w_up", grad_w_up, inner, cols, pdt, dev)
+    ddp, dds = _like(what, "grad_w_down", grad_w_down, cols, inner, pdt, dev)
+    act = _activation(what, activation)
+    wp, wb = _work(what, workspace, dev)
+    handle = _on(what, dev, stream)
+    _check(lib().fsdp_gated_ffn_grad(rows, cols, inner, gp, gs, xp, xs, wgp, wgs, wup, wus, wdp, wds, kg, kgs, ku, kus, act, dxp,
+                                     dxs, pdt, int(accumulate), dgp, dgs, dup, dus, ddp, dds, wp, wb, handle))
+
+
+def fsdp_orthogonalize_workspace(rows, cols):
+    """Bytes of the workspace that fsdp_orthogonalize needs."""
+    b = ctypes.c_size_t()
+    _check(lib().fsdp_orthogonalize_workspace(rows, cols, ctypes.byref(b)))
+    return b.value
+
+
+def fsdp_orthogonalize(x, out, workspace, steps=5, coefficients=(3.4445, -4.7750, 2.0315), scale=1.0, eps=1e-7, stream=None):
+    """out = scale * X after `steps` Newton-Schulz steps from X = x / (|x| + eps):
+    with A = X X^T, X <- a X + (b A + c A A) X. x: a matrix of float32 or
+    bfloat16; out: the same shape in bfloat16. workspace: a tensor of at least
+    fsdp_orthogonalize_workspace(rows, cols) bytes."""
+    what = "orthogonalize"
+    xp, rows, cols, xs, dt, dev = _matrix(what, "x", x)
+    op, os_ = _like(what, "out", out, rows, cols, FSDP_BF16, dev)
+    a, b, c = coefficients
+    wp, wb = _work(what, workspace, dev)
+    handle = _on(what, dev, stream)
+    _check(lib().fsdp_orthogonalize(rows, cols, dt, xp, xs, steps, a, b, c, scale, eps, op, os_, wp, wb, handle))

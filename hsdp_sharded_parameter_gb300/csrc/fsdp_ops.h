@@ -1,5 +1,5 @@
-// Launch interface of the training operators (embedding, dropout, layer
-// norm): what the C-ABI entry points (fsdp_ops_capi.cpp) hand to the kernels
+// Launch interface of the training operators (embedding, dropout, layer norm,
+// gated feed-forward, orthogonalised updates): what the C-ABI entry points (fsdp_ops_capi.cpp) hand to the kernels
 // once the arguments are checked. Not installed.
 #pragma once
 
@@ -79,6 +79,29 @@ struct NormGradArgs {
     Mask mask;
 };
 
+struct FfnArgs {
+    int64_t tokens, hidden, inner;
+    int act;
+    Mat x, w_gate, w_up, w_down, gate, up, out;  // gate.data, up.data may both be nullptr
+    char* work;
+};
+
+struct FfnGradArgs {
+    int64_t tokens, hidden, inner;
+    int act, accumulate;
+    Mat grad, x, w_gate, w_up, w_down, gate, up, grad_x, grad_gate, grad_up, grad_down;
+    char* work;
+};
+
+struct OrthoArgs {
+    int64_t rows, cols;
+    Mat x, out;
+    int steps;
+    float a, b, c, scale;
+    double eps;
+    char* work;
+};
+
 // SMs of the current device.
 int sm_count();
 // Lets a kernel take up to `bytes` of dynamic shared memory on the current
@@ -93,11 +116,24 @@ size_t embedding_grad_bytes(int64_t n, int64_t vocab, int64_t cols);
 size_t embedding_grad_most_bytes(int64_t n, int64_t vocab, int64_t cols);
 size_t norm_grad_bytes(int64_t rows, int64_t cols);
 
+size_t ffn_bytes(const FfnArgs& a);
+size_t ffn_most_bytes(int64_t tokens, int64_t hidden, int64_t inner, bool aligned);
+size_t ffn_grad_bytes(const FfnGradArgs& a);
+size_t ffn_grad_most_bytes(int64_t tokens, int64_t hidden, int64_t inner, bool aligned);
+size_t ortho_bytes(int64_t rows, int64_t cols);
+
 // Each enqueues its kernels (counting them) and returns the launches' error.
 cudaError_t launch_embedding(int table_dt, int out_dt, const EmbeddingArgs& a, cudaStream_t s);
 cudaError_t launch_embedding_grad(int grad_dt, int table_dt, const EmbeddingGradArgs& a, cudaStream_t s);
 cudaError_t launch_dropout(int dt, const DropoutArgs& a, cudaStream_t s);
 cudaError_t launch_norm(int dt, const NormArgs& a, cudaStream_t s);
 cudaError_t launch_norm_grad(int dt, int param_grad_dt, const NormGradArgs& a, cudaStream_t s);
+cudaError_t launch_ffn(const FfnArgs& a, cudaStream_t s);
+cudaError_t launch_ffn_grad(int param_grad_dt, const FfnGradArgs& a, cudaStream_t s);
+cudaError_t launch_ortho(int dt, const OrthoArgs& a, cudaStream_t s);
+// Whether a wait inside an operator's kernel has run out since the last
+// question, after what the stream holds.
+cudaError_t ffn_gave_up(int* value, cudaStream_t s);
+cudaError_t ortho_gave_up(int* value, cudaStream_t s);
 
 }  // namespace fsdp

@@ -1,5 +1,6 @@
 // C-ABI entry points of the training operators: argument checks and the
-// hand-over to the kernels (fsdp_embedding.cu, fsdp_dropout.cu, fsdp_norm.cu).
+// hand-over to the kernels (fsdp_embedding.cu, fsdp_dropout.cu, fsdp_norm.cu,
+// fsdp_ffn.cu, fsdp_ortho.cu).
 #include <cmath>
 #include <cstdint>
 #include <initializer_list>
@@ -120,6 +121,28 @@ int launched(cudaError_t e, const char* what) {
     if (e == cudaSuccess) return FSDP_OK;
     (void)cudaGetLastError();  // reported here, not by the caller's next call
     return set_error(FSDP_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
+}
+
+// Sizes of the products' operators: tiles are numbered and placed in 32 bits.
+constexpr int64_t kMaxProduct = INT32_MAX - 512;
+
+int check_product(const char* what, std::initializer_list<int64_t> sizes) {
+    for (const int64_t n : sizes)
+        if (n < 0 || n > kMaxProduct) return bad(what, "a size is negative or too large");
+    return FSDP_OK;
+}
+
+int check_activation(const char* what, int act) {
+    return act == FSDP_SILU || act == FSDP_GELU || act == FSDP_RELU ? FSDP_OK : bad(what, "unknown activation");
+}
+
+// No output may be another operand's memory.
+int check_apart(const char* what, std::initializer_list<Operand> ops) {
+    for (const Operand& o : ops)
+        if (o.output && o.data)
+            for (const Operand& p : ops)
+                if (&p != &o && p.data == o.data) return bad(what, std::string(o.name) + " is another operand's memory");
+    return FSDP_OK;
 }
 
 Mat mat(const void* data, int64_t stride) { return Mat{const_cast<void*>(data), stride}; }
@@ -262,6 +285,122 @@ int fsdp_layer_norm_grad(int64_t rows, int64_t cols, int dt, const void* grad_ou
                       mean, rstd, param_dt, weight, grad_weight, grad_bias, accumulate ? 1 : 0, static_cast<float*>(workspace), {}};
     FSDP_TRY(make_mask(what, p, seed, draw, cols, a.mask));
     return launched(launch_norm_grad(dt, param_grad_dt, a, stream), what);
+}
+
+int fsdp_operators_status(fsdp_stream_t stream, int* status) {
+    const char* what = "operators_status";
+    clear_error();
+    if (!status) return bad(what, "status is NULL");
+    int ffn = 0, ortho = 0;
+    FSDP_TRY(launched(ffn_gave_up(&ffn, stream), what));
+    FSDP_TRY(launched(ortho_gave_up(&ortho, stream), what));
+    *status = ffn || ortho ? 1 : 0;
+    return FSDP_OK;
+}
+
+int fsdp_gated_ffn_workspace(int64_t tokens, int64_t hidden, int64_t inner, int aligned, size_t* bytes) {
+    const char* what = "gated_ffn_workspace";
+    clear_error();
+    if (!bytes) return bad(what, "bytes is NULL");
+    FSDP_TRY(check_product(what, {tokens, hidden, inner}));
+    *bytes = ffn_most_bytes(tokens, hidden, inner, aligned != 0);
+    return FSDP_OK;
+}
+
+int fsdp_gated_ffn(int64_t tokens, int64_t hidden, int64_t inner, const void* x, int64_t x_stride, const void* w_gate,
+                   int64_t w_gate_stride, const void* w_up, int64_t w_up_stride, const void* w_down,
+                   int64_t w_down_stride, int activation, void* gate, int64_t gate_stride, void* up,
+                   int64_t up_stride, void* out, int64_t out_stride, void* workspace, size_t workspace_bytes,
+                   fsdp_stream_t stream) {
+    const char* what = "gated_ffn";
+    clear_error();
+    FSDP_TRY(check_product(what, {tokens, hidden, inner}));
+    FSDP_TRY(check_activation(what, activation));
+    const int dt = FSDP_BF16;
+    const Operand ox = {"x", x, x_stride, dt, tokens, false, false}, og = {"w_gate", w_gate, w_gate_stride, dt, inner, false, false},
+                  ou = {"w_up", w_up, w_up_stride, dt, inner, false, false},
+                  od = {"w_down", w_down, w_down_stride, dt, hidden, false, false},
+                  kg = {"gate", gate, gate_stride, dt, tokens, true, true}, ku = {"up", up, up_stride, dt, tokens, true, true},
+                  oo = {"out", out, out_stride, dt, tokens, true, false};
+    FSDP_TRY(check_operands(what, hidden, {ox, og, ou, oo}));
+    FSDP_TRY(check_operands(what, inner, {od, kg, ku}));
+    if (tokens > 0 && inner > 0 && !gate != !up) return bad(what, "gate and up: one of them is NULL");
+    FSDP_TRY(check_apart(what, {ox, og, ou, od, kg, ku, oo}));
+    const FfnArgs a = {tokens, hidden, inner, activation, mat(x, x_stride), mat(w_gate, w_gate_stride), mat(w_up, w_up_stride),
+                       mat(w_down, w_down_stride), mat(gate, gate_stride), mat(up, up_stride), mat(out, out_stride),
+                       static_cast<char*>(workspace)};
+    FSDP_TRY(check_work(what, workspace, workspace_bytes, ffn_bytes(a)));
+    return launched(launch_ffn(a, stream), what);
+}
+
+int fsdp_gated_ffn_grad_workspace(int64_t tokens, int64_t hidden, int64_t inner, int aligned, size_t* bytes) {
+    const char* what = "gated_ffn_grad_workspace";
+    clear_error();
+    if (!bytes) return bad(what, "bytes is NULL");
+    FSDP_TRY(check_product(what, {tokens, hidden, inner}));
+    *bytes = ffn_grad_most_bytes(tokens, hidden, inner, aligned != 0);
+    return FSDP_OK;
+}
+
+int fsdp_gated_ffn_grad(int64_t tokens, int64_t hidden, int64_t inner, const void* grad_out, int64_t grad_out_stride,
+                        const void* x, int64_t x_stride, const void* w_gate, int64_t w_gate_stride, const void* w_up,
+                        int64_t w_up_stride, const void* w_down, int64_t w_down_stride, const void* gate,
+                        int64_t gate_stride, const void* up, int64_t up_stride, int activation, void* grad_x,
+                        int64_t grad_x_stride, int param_grad_dt, int accumulate, void* grad_w_gate,
+                        int64_t grad_w_gate_stride, void* grad_w_up, int64_t grad_w_up_stride, void* grad_w_down,
+                        int64_t grad_w_down_stride, void* workspace, size_t workspace_bytes, fsdp_stream_t stream) {
+    const char* what = "gated_ffn_grad";
+    clear_error();
+    FSDP_TRY(check_product(what, {tokens, hidden, inner}));
+    FSDP_TRY(check_activation(what, activation));
+    const int dt = FSDP_BF16;
+    const Operand og = {"grad_out", grad_out, grad_out_stride, dt, tokens, false, false}, ox = {"x", x, x_stride, dt, tokens, false, false},
+                  wg = {"w_gate", w_gate, w_gate_stride, dt, inner, false, false},
+                  wu = {"w_up", w_up, w_up_stride, dt, inner, false, false},
+                  wd = {"w_down", w_down, w_down_stride, dt, hidden, false, false},
+                  kg = {"gate", gate, gate_stride, dt, tokens, false, false}, ku = {"up", up, up_stride, dt, tokens, false, false},
+                  gx = {"grad_x", grad_x, grad_x_stride, dt, tokens, true, false},
+                  gg = {"grad_w_gate", grad_w_gate, grad_w_gate_stride, param_grad_dt, inner, true, false},
+                  gu = {"grad_w_up", grad_w_up, grad_w_up_stride, param_grad_dt, inner, true, false},
+                  gd = {"grad_w_down", grad_w_down, grad_w_down_stride, param_grad_dt, hidden, true, false};
+    FSDP_TRY(check_operands(what, hidden, {og, ox, wg, wu, gx, gg, gu}));
+    FSDP_TRY(check_operands(what, inner, {wd, kg, ku, gd}));
+    FSDP_TRY(check_apart(what, {og, ox, wg, wu, wd, kg, ku, gx, gg, gu, gd}));
+    const FfnGradArgs a = {tokens, hidden, inner, activation, accumulate ? 1 : 0, mat(grad_out, grad_out_stride), mat(x, x_stride),
+                           mat(w_gate, w_gate_stride), mat(w_up, w_up_stride), mat(w_down, w_down_stride), mat(gate, gate_stride),
+                           mat(up, up_stride), mat(grad_x, grad_x_stride), mat(grad_w_gate, grad_w_gate_stride),
+                           mat(grad_w_up, grad_w_up_stride), mat(grad_w_down, grad_w_down_stride), static_cast<char*>(workspace)};
+    FSDP_TRY(check_work(what, workspace, workspace_bytes, ffn_grad_bytes(a)));
+    return launched(launch_ffn_grad(param_grad_dt, a, stream), what);
+}
+
+int fsdp_orthogonalize_workspace(int64_t rows, int64_t cols, size_t* bytes) {
+    const char* what = "orthogonalize_workspace";
+    clear_error();
+    if (!bytes) return bad(what, "bytes is NULL");
+    FSDP_TRY(check_product(what, {rows, cols}));
+    *bytes = ortho_bytes(rows, cols);
+    return FSDP_OK;
+}
+
+int fsdp_orthogonalize(int64_t rows, int64_t cols, int dt, const void* x, int64_t x_stride, int steps, double a,
+                       double b, double c, double scale, double eps, void* out, int64_t out_stride, void* workspace,
+                       size_t workspace_bytes, fsdp_stream_t stream) {
+    const char* what = "orthogonalize";
+    clear_error();
+    FSDP_TRY(check_product(what, {rows, cols}));
+    const Operand ox = {"x", x, x_stride, dt, rows, false, false}, oo = {"out", out, out_stride, FSDP_BF16, rows, true, false};
+    FSDP_TRY(check_operands(what, cols, {ox, oo}));
+    FSDP_TRY(check_apart(what, {ox, oo}));
+    if (steps < 1 || steps > 64) return bad(what, "steps is not in [1, 64]");
+    for (const double v : {a, b, c})
+        if (!(std::fabs(v) <= 256.0)) return bad(what, "a coefficient is not in [-256, 256]");
+    FSDP_TRY(check_float(what, "scale", scale));
+    if (!(eps >= 0.0 && std::isfinite(eps))) return bad(what, "eps is negative or not finite");
+    FSDP_TRY(check_work(what, workspace, workspace_bytes, ortho_bytes(rows, cols)));
+    const OrthoArgs args = {rows, cols, mat(x, x_stride), mat(out, out_stride), steps, (float)a, (float)b, (float)c, (float)scale, eps,
+                            static_cast<char*>(workspace)};
+    return launched(launch_ortho(dt, args, stream), what);
 }
 
 }  // extern "C"

@@ -1,0 +1,421 @@
+// Orthogonalisation of an update by Newton-Schulz products.
+//
+// The iterate X is kept in two binary16 planes, X = 2^-sx (hi + 2^-11 lo), of
+// which the products take hi. A product with binary16 factors is off by 2^-12
+// of its factors' sizes, and the iteration lifts small singular values by up
+// to a^steps (485 times), and what is off in their directions with them. So
+// the term that lifts them, shift * X, is added in binary32 from both planes,
+// and the product only brings (b A + c A A + (a - shift) I) X, where A is small
+// in those directions and damps what is off. (Five steps against 64 bits, in
+// the 2-norm, a few strong directions over 3% or 0.1% of noise: 0.002; with
+// one plane 0.02 and 0.04; in bfloat16 0.17 and 0.34. Noise alone 0.002, 0.002
+// and 0.011. Rounding the result to bfloat16 alone is 0.0017.) In the last two
+// steps the singular values are near one, and a shift near one leaves the
+// product the smaller part.
+#include <algorithm>
+#include <cmath>
+#include <utility>
+
+#include "fsdp_gemm.cuh"
+
+namespace fsdp {
+namespace {
+
+constexpr int kSquareBlocks = 304, kSquareThreads = 256;
+
+__device__ __forceinline__ uint32_t half_bits(float v) { return (uint32_t)__half_as_ushort(__float2half_rn(v)); }
+__device__ __forceinline__ float half_value(uint32_t b) { return __half2float(__ushort_as_half((unsigned short)b)); }
+__device__ __forceinline__ void round_half(const Cols& v, Raw<uint16_t>& r) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.w[i] = half_bits(v.p[i].x) | half_bits(v.p[i].y) << 16;
+}
+__device__ __forceinline__ Cols widened_half(const Raw<uint16_t>& r) {
+    Cols v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v.p[i] = make_float2(half_value(r.w[i] & 0xffffu), half_value(r.w[i] >> 16));
+    return v;
+}
+__device__ __forceinline__ uint16_t* at(const Mat& m, int64_t row, int64_t col) {
+    return static_cast<uint16_t*>(m.data) + row * m.stride + col;
+}
+__device__ __forceinline__ void put_half(const Mat& m, int64_t row, int64_t col, int n, const Cols& v) {
+    Raw<uint16_t> r;
+    round_half(v, r);
+    store_granule(at(m, row, col), r, n);
+}
+constexpr float kLow = 2048.0f;  // the second plane's scale
+// Both planes of values of the first plane's scale.
+__device__ __forceinline__ void put_planes(const Mat& hi, const Mat& lo, int64_t row, int64_t col, int n, const Cols& v) {
+    Raw<uint16_t> r;
+    round_half(v, r);
+    store_granule(at(hi, row, col), r, n);
+    const Cols rest = (v + widened_half(r) * all(-1.0f)) * all(kLow);
+    put_half(lo, row, col, n, rest);
+}
+
+// ------------------------------------------------------- the first iterate
+
+// A block's sums of squares, of values by their size, so that no square
+// overflows or vanishes: those of at least 2^60 by 2^-64, those below 2^-50 by
+// 2^64 (Blue, "A portable Fortran program to find the Euclidean norm of a
+// vector", 1978).
+template <typename T>
+__global__ void __launch_bounds__(kSquareThreads) square_kernel(Mat x, int64_t rows, int64_t cols, float* parts) {
+    wait_for_previous();
+    const int64_t per = (cols + kGran - 1) / kGran, all_granules = rows * per;
+    float sum[3] = {0.0f, 0.0f, 0.0f};
+    for (int64_t g = (int64_t)blockIdx.x * kSquareThreads + threadIdx.x; g < all_granules; g += (int64_t)kSquareBlocks * kSquareThreads) {
+        const int64_t row = g / per, i = g - row * per;
+        Raw<T> r;
+        load_granule(r, static_cast<const T*>(x.data) + row * x.stride, i * kGran, granule_cols(i, cols));
+        const Cols v = widened(r);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float f = v.get(e), m = fabsf(f);
+            const int which = m >= 0x1p60f ? 2 : (m < 0x1p-50f ? 0 : 1);
+            const float q = which == 2 ? f * 0x1p-64f : (which == 0 ? f * 0x1p64f : f);
+            sum[0] = which == 0 ? __fmaf_rn(q, q, sum[0]) : sum[0];
+            sum[2] = which == 2 ? __fmaf_rn(q, q, sum[2]) : sum[2];
+            sum[1] = which == 1 ? __fmaf_rn(q, q, sum[1]) : sum[1];  // NaN too
+        }
+    }
+    __shared__ float box[3][kSquareThreads / 32];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        sum[k] = warp_sum(sum[k]);
+        if (threadIdx.x % 32 == 0) box[k][threadIdx.x / 32] = sum[k];
+    }
+    __syncthreads();
+    if (threadIdx.x < 3) {
+        float total = 0.0f;
+        for (int w = 0; w < kSquareThreads / 32; ++w) total += box[threadIdx.x][w];
+        parts[threadIdx.x * kSquareBlocks + blockIdx.x] = total;
+    }
+}
+
+// lift / (|x| + eps) from the parts, as a product of two factors neither of
+// which leaves binary32's range. All threads of a block of at least 96 take
+// part.
+__device__ __forceinline__ float2 norm_factor(const float* parts, double eps, float lift) {
+    __shared__ double sums[3];
+    __shared__ float2 factor;
+    if (threadIdx.x < 96) {
+        double s = 0.0;
+        for (int i = threadIdx.x % 32; i < kSquareBlocks; i += 32) s += (double)parts[threadIdx.x / 32 * kSquareBlocks + i];
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
+        if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = s;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const double norm = sqrt(sums[0] * 0x1p-128 + sums[1] + sums[2] * 0x1p128);
+        const double f = (double)lift / (norm + eps);
+        int e = 0;
+        const double m = frexp(f, &e);
+        factor = isfinite(f) ? make_float2(ldexpf(1.0f, e / 2), (float)ldexp(m, e - e / 2)) : make_float2((float)f, 1.0f);
+    }
+    __syncthreads();
+    return factor;
+}
+
+// X = x / (|x| + eps) as two planes scaled by `lift`.
+template <typename T>
+__global__ void __launch_bounds__(256) planes_kernel(Mat x, int64_t rows, int64_t cols, const float* parts, double eps, float lift, Mat hi,
+                                                     Mat lo) {
+    wait_for_previous();
+    const float2 f = norm_factor(parts, eps, lift);
+    const int64_t per = (cols + kGran - 1) / kGran, all_granules = rows * per;
+    for (int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x; g < all_granules; g += (int64_t)gridDim.x * 256) {
+        const int64_t row = g / per, i = g - row * per;
+        const int n = granule_cols(i, cols);
+        Raw<T> r;
+        load_granule(r, static_cast<const T*>(x.data) + row * x.stride, i * kGran, n);
+        put_planes(hi, lo, row, i * kGran, n, widened(r) * all(f.x) * all(f.y));
+    }
+}
+
+// ------------------------------------------------------ one short side
+//
+// With at most 64 rows (or columns) everything after the first A happens in
+// p x p matrices, which are polynomials of A and commute: with M = a I + b A +
+// c A A a step is P <- M P, A <- M M A, and at the end X = P X_0. All of it in
+// binary32, in one block. (So few values average no rounding: in binary16 a
+// 1 x 1 matrix is 0.007 off.)
+constexpr int kSide = 64, kChunk = 64, kSidePitch = kSide + 4, kGramBlocks = 64, kNarrowThreads = 256;
+constexpr int kSideValues = kSide * kSidePitch;
+
+__device__ __forceinline__ float value_of(const float* p) { return *p; }
+__device__ __forceinline__ float value_of(const uint16_t* p) { return bf16_to_f32(*p); }
+
+// kChunk columns of X (rows, where tall) from j0 on, to[j][i].
+template <typename T>
+__device__ __forceinline__ void bring_chunk(float* to, const Mat& x, int tall, int p, int64_t q, int64_t j0, float2 f) {
+    const T* data = static_cast<const T*>(x.data);
+    for (int c = threadIdx.x; c < kSide * kChunk; c += kNarrowThreads) {
+        const int i = tall ? c % kSide : c / kChunk, j = tall ? c / kSide : c % kChunk;
+        float v = 0.0f;
+        if (i < p && j0 + j < q) v = value_of(tall ? data + (j0 + j) * x.stride + i : data + i * x.stride + j0 + j) * f.x * f.y;
+        to[j * kSidePitch + i] = v;
+    }
+}
+
+// A thread's 4 x 4 values of sum over k of a[k][i] b[k][j].
+__device__ __forceinline__ void small_product(float (&s)[4][4], const float* a, const float* b, int k_end, int i0, int j0) {
+#pragma unroll 4
+    for (int k = 0; k < k_end; ++k) {
+        const float4 u = *reinterpret_cast<const float4*>(a + k * kSidePitch + i0), v = *reinterpret_cast<const float4*>(b + k * kSidePitch + j0);
+        const float x[4] = {u.x, u.y, u.z, u.w}, y[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) s[r][c] = __fmaf_rn(x[r], y[c], s[r][c]);
+    }
+}
+
+// A block's share of A = X X^T.
+template <typename T>
+__global__ void __launch_bounds__(kNarrowThreads) narrow_gram_kernel(Mat x, int tall, int p, int64_t q, const float* parts, double eps,
+                                                                     float* grams) {
+    __shared__ __align__(16) float chunk[kChunk * kSidePitch];
+    wait_for_previous();
+    const float2 f = norm_factor(parts, eps, 1.0f);
+    const int i0 = threadIdx.x / 16 * 4, j0 = threadIdx.x % 16 * 4;
+    float s[4][4] = {};
+    for (int64_t j = (int64_t)blockIdx.x * kChunk; j < q; j += (int64_t)gridDim.x * kChunk) {
+        bring_chunk<T>(chunk, x, tall, p, q, j, f);
+        __syncthreads();
+        if (i0 < p && j0 < p) small_product(s, chunk, chunk, kChunk, i0, j0);
+        __syncthreads();
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        *reinterpret_cast<float4*>(grams + ((int64_t)blockIdx.x * kSide + i0 + r) * kSide + j0) = make_float4(s[r][0], s[r][1], s[r][2], s[r][3]);
+}
+
+// The steps on A, from its parts; P times scale to `poly`.
+__global__ void __launch_bounds__(kNarrowThreads) narrow_steps_kernel(const float* grams, int n_parts, int p, int steps, float a, float b, float c,
+                                                                      float scale, float* poly) {
+    extern __shared__ __align__(16) float box[];
+    float *A = box, *M = box + kSideValues, *P = box + 2 * kSideValues, *S = box + 3 * kSideValues;
+    wait_for_previous();
+    for (int e = threadIdx.x; e < kSide * kSide; e += kNarrowThreads) {
+        float sum = 0.0f;
+        for (int k = 0; k < n_parts; ++k) sum += grams[(int64_t)k * kSide * kSide + e];
+        A[e / kSide * kSidePitch + e % kSide] = sum;
+        P[e / kSide * kSidePitch + e % kSide] = e / kSide == e % kSide ? 1.0f : 0.0f;
+    }
+    __syncthreads();
+    const int i0 = threadIdx.x / 16 * 4, j0 = threadIdx.x % 16 * 4, k_end = (p + 3) / 4 * 4;
+    const bool in = i0 < p && j0 < p;
+    auto keep = [&](float* to, const float (&s)[4][4]) {
+        if (!in) return;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) *reinterpret_cast<float4*>(to + (i0 + r) * kSidePitch + j0) = make_float4(s[r][0], s[r][1], s[r][2], s[r][3]);
+    };
+    for (int t = 0; t < steps; ++t) {
+        float s[4][4] = {}, m[4][4] = {};
+        if (in) small_product(s, A, A, k_end, i0, j0);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                m[r][e] = __fmaf_rn(c, s[r][e], __fmaf_rn(b, A[(i0 + r) * kSidePitch + j0 + e], i0 + r == j0 + e ? a : 0.0f));
+        keep(M, m);
+        __syncthreads();
+        float u[4][4] = {}, v[4][4] = {};
+        if (in) small_product(u, M, P, k_end, i0, j0);
+        if (in) small_product(v, M, M, k_end, i0, j0);
+        keep(S, v);
+        __syncthreads();
+        keep(P, u);
+        float w[4][4] = {};
+        if (in) small_product(w, S, A, k_end, i0, j0);
+        __syncthreads();
+        keep(A, w);
+        __syncthreads();
+    }
+    for (int e = threadIdx.x; e < kSide * kSide; e += kNarrowThreads)
+        poly[e] = e / kSide < p && e % kSide < p ? P[e / kSide * kSidePitch + e % kSide] * scale : 0.0f;
+}
+
+// out = P X_0, kChunk columns (rows, where tall) at a time.
+template <typename T>
+__global__ void __launch_bounds__(kNarrowThreads) narrow_apply_kernel(Mat x, int tall, int p, int64_t q, const float* parts, double eps,
+                                                                      const float* poly, Mat out) {
+    __shared__ __align__(16) float chunk[kChunk * kSidePitch], box[kSideValues];
+    wait_for_previous();
+    const float2 f = norm_factor(parts, eps, 1.0f);
+    for (int e = threadIdx.x; e < kSide * kSide; e += kNarrowThreads) box[e % kSide * kSidePitch + e / kSide] = poly[e];
+    const int i0 = threadIdx.x / 16 * 4, j0 = threadIdx.x % 16 * 4;
+    for (int64_t j = (int64_t)blockIdx.x * kChunk; j < q; j += (int64_t)gridDim.x * kChunk) {
+        // [k][j]: the chunk transposed
+        const T* data = static_cast<const T*>(x.data);
+        __syncthreads();
+        for (int c = threadIdx.x; c < kSide * kChunk; c += kNarrowThreads) {
+            const int i = tall ? c % kSide : c / kChunk, jj = tall ? c / kSide : c % kChunk;
+            float v = 0.0f;
+            if (i < p && j + jj < q) v = value_of(tall ? data + (j + jj) * x.stride + i : data + i * x.stride + j + jj) * f.x * f.y;
+            chunk[i * kSidePitch + jj] = v;
+        }
+        __syncthreads();
+        if (i0 >= p) continue;
+        float s[4][4] = {};
+        small_product(s, box, chunk, p, i0, j0);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int i = i0 + r;
+                const int64_t jj = j + j0 + c;
+                if (i < p && jj < q) {
+                    uint16_t* to = tall ? at(out, jj, i) : at(out, i, jj);
+                    *to = (uint16_t)f32_to_bf16(s[r][c]);
+                }
+            }
+    }
+}
+
+// -------------------------------------------------------------- epilogues
+
+// A = X X^T.
+struct Gram {
+    Mat out;
+    float scale;
+    __device__ __forceinline__ void operator()(int64_t row, int64_t col, int n, const Cols& v, const Cols&) const {
+        put_half(out, row, col, n, v * all(scale));
+    }
+};
+
+// c A A + b A + d I.
+struct Poly {
+    Mat a, out;
+    float square, linear, diagonal;
+    __device__ __forceinline__ void operator()(int64_t row, int64_t col, int n, const Cols& v, const Cols&) const {
+        Raw<uint16_t> r;
+        load_granule(r, at(a, row, col), 0, n);
+        Cols s = fma(v, all(square), widened_half(r) * all(linear));
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (col + e == row) s.set(e, s.get(e) + diagonal);
+        put_half(out, row, col, n, s);
+    }
+};
+
+// X <- shift X + D, into the planes, or at the end into the caller's matrix.
+struct Next {
+    Mat hi, lo, next, out;  // out.data: the caller's
+    float scale, shift;
+    __device__ __forceinline__ void operator()(int64_t row, int64_t col, int n, const Cols& v, const Cols&) const {
+        Raw<uint16_t> r;
+        load_granule(r, at(hi, row, col), 0, n);
+        Cols x = widened_half(r);
+        load_granule(r, at(lo, row, col), 0, n);
+        x = fma(widened_half(r), all(1.0f / kLow), x);
+        x = fma(v, all(scale), x * all(shift));
+        if (!out.data) {
+            put_planes(next, lo, row, col, n, x);
+        } else {
+            round_to(x, r);
+            store_granule(at(out, row, col), r, n);
+        }
+    }
+};
+
+int64_t padded(int64_t n) { return (n + 7) / 8 * 8; }
+size_t room(int64_t rows, int64_t cols) { return (size_t)((rows * padded(cols) * 2 + 255) / 256 * 256); }
+constexpr size_t kPartsRoom = (3 * kSquareBlocks * 4 + 255) / 256 * 256;
+
+constexpr size_t kNarrowRoom = (size_t)(kGramBlocks + 1) * kSide * kSide * 4;
+
+template <typename T>
+cudaError_t narrow(const OrthoArgs& a, cudaStream_t s) {
+    const bool tall = a.rows > a.cols;
+    const int p = (int)(tall ? a.cols : a.rows);
+    const int64_t q = tall ? a.rows : a.cols, chunks = (q + kChunk - 1) / kChunk;
+    const float* parts = reinterpret_cast<const float*>(a.work);
+    float* grams = reinterpret_cast<float*>(a.work + kPartsRoom);
+    float* poly = grams + (size_t)kGramBlocks * kSide * kSide;
+    const int n_parts = (int)std::min<int64_t>(chunks, kGramBlocks);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(narrow_steps_kernel), 4 * kSideValues * 4, done);
+    if (e == cudaSuccess) e = launch_next(narrow_gram_kernel<T>, dim3(n_parts), kNarrowThreads, 0, s, a.x, (int)tall, p, q, parts, a.eps, grams);
+    count_launch();
+    if (e == cudaSuccess)
+        e = launch_next(narrow_steps_kernel, dim3(1), kNarrowThreads, 4 * kSideValues * 4, s, (const float*)grams, n_parts, p, a.steps, a.a, a.b, a.c,
+                        a.scale, poly);
+    count_launch();
+    const int grid = (int)std::min<int64_t>(chunks, 4 * sm_count());
+    if (e == cudaSuccess)
+        e = launch_next(narrow_apply_kernel<T>, dim3(grid), kNarrowThreads, 0, s, a.x, (int)tall, p, q, parts, a.eps, (const float*)poly, a.out);
+    count_launch();
+    return e;
+}
+
+int log2_near(double v) { return (int)std::nearbyint(std::log2(v)); }
+
+}  // namespace
+
+size_t ortho_bytes(int64_t rows, int64_t cols) {
+    if (rows == 0 || cols == 0) return 0;
+    const int64_t p = rows < cols ? rows : cols;
+    if (p <= kSide) return kPartsRoom + kNarrowRoom;
+    return kPartsRoom + 3 * room(rows, cols) + 2 * room(p, p);
+}
+
+cudaError_t launch_ortho(int dt, const OrthoArgs& a, cudaStream_t s) {
+    if (a.rows == 0 || a.cols == 0) return cudaSuccess;
+    const bool tall = a.rows > a.cols;
+    const int64_t p = tall ? a.cols : a.rows, q = tall ? a.rows : a.cols;
+    const size_t plane = room(a.rows, a.cols);
+    const int64_t ld = padded(a.cols), lp = padded(p);
+    float* parts = reinterpret_cast<float*>(a.work);
+    char* w = a.work + kPartsRoom;
+    Mat hi = {w, ld}, next = {w + plane, ld};
+    const Mat lo = {w + 2 * plane, ld}, gram = {w + 3 * plane, lp}, poly = {w + 3 * plane + room(p, p), lp};
+    // Scales by powers of two that keep values in binary16's normal range: X's
+    // elements are about 1/sqrt(p q) at first and 1/sqrt(q) at the end, never
+    // above about 1.2; A's diagonal about 1/p at first; the polynomial's at most
+    // |a| + 1.5 |b| + 2.25 |c|.
+    const int sx = log2_near(std::sqrt((double)q));
+    const int sa = std::min(13, log2_near((double)p));
+    const double most = std::fabs(a.a) + 1.5 * std::fabs(a.b) + 2.25 * std::fabs(a.c);
+    const int sb = std::min(sa, 15 - (int)std::ceil(std::log2(std::max(most, 1.0))));
+    const float lift = std::ldexp(1.0f, sx);
+    if (dt == FSDP_F32)
+        square_kernel<float><<<kSquareBlocks, kSquareThreads, 0, s>>>(a.x, a.rows, a.cols, parts);
+    else
+        square_kernel<uint16_t><<<kSquareBlocks, kSquareThreads, 0, s>>>(a.x, a.rows, a.cols, parts);
+    count_launch();
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    if (p <= kSide) return dt == FSDP_F32 ? narrow<float>(a, s) : narrow<uint16_t>(a, s);
+    const int64_t granules = a.rows * ((a.cols + kGran - 1) / kGran);
+    const int grid = (int)std::min<int64_t>((granules + 255) / 256, 8 * sm_count());
+    e = dt == FSDP_F32 ? launch_next(planes_kernel<float>, dim3(grid), 256, 0, s, a.x, a.rows, a.cols, (const float*)parts, a.eps, lift, hi, lo)
+                       : launch_next(planes_kernel<uint16_t>, dim3(grid), 256, 0, s, a.x, a.rows, a.cols, (const float*)parts, a.eps, lift, hi, lo);
+    count_launch();
+    for (int i = 0; i < a.steps && e == cudaSuccess; ++i) {
+        const float shift = i + 2 < a.steps ? a.a : 0.5f * (1.0f + a.a);
+        const Product square = {p, p, 1, {q, 0}, {hi, {}}, {hi, {}}, tall, tall, 1, 0};
+        e = launch_product(square, Gram{gram, std::ldexp(1.0f, sa - 2 * sx)}, s, false);
+        const Product again = {p, p, 1, {p, 0}, {gram, {}}, {gram, {}}, 0, 0, 1, 0};
+        const Poly mix = {gram, poly, std::ldexp(a.c, sb - 2 * sa), std::ldexp(a.b, sb - sa), std::ldexp(a.a - shift, sb)};
+        if (e == cudaSuccess) e = launch_product(again, mix, s, false);
+        Product apply = {a.rows, a.cols, 1, {p, 0}, {poly, {}}, {hi, {}}, 0, 1, 1, 0};
+        if (tall) {
+            apply.a[0] = hi;
+            apply.b[0] = poly;
+            apply.b_mn = 0;
+        }
+        const bool last = i + 1 == a.steps;
+        const float out = last ? std::ldexp(a.scale, -sx) : 1.0f;
+        if (e == cudaSuccess)
+            e = launch_product(apply, Next{hi, lo, next, last ? a.out : Mat{nullptr, 0}, std::ldexp(out, -sb), shift * out}, s, false);
+        std::swap(hi, next);
+    }
+    return e;
+}
+
+cudaError_t ortho_gave_up(int* value, cudaStream_t s) { return take_gave_up(value, s); }
+
+}  // namespace fsdp

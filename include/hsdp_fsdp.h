@@ -499,6 +499,92 @@ int fsdp_layer_norm_grad(int64_t rows, int64_t cols, int dt, const void* grad_ou
                          int64_t grad_x_stride, int param_grad_dt, void* grad_weight, void* grad_bias,
                          void* workspace, size_t workspace_bytes, fsdp_stream_t stream);
 
+/* ------------------------------------------ products of a feed-forward block */
+
+/* The gated feed-forward block of a transformer layer, its gradient, and the
+ * orthogonalisation of a matrix's update: the operators whose time is matrix
+ * products, on the tensor cores. What is said of the training operators above
+ * holds here, with these differences:
+ *   - Types: matrices are bfloat16 where no type is an argument; sums are in
+ *     binary32. What passes from one product to the next is rounded to 16 bits
+ *     on the way, as each call says.
+ *   - Workspaces: an operand whose rows do not all start on the 16-byte grid
+ *     (or overlap) is first copied to the workspace, which has to hold it; the
+ *     _workspace functions take a flag for whether every matrix operand is on
+ *     the grid (its pointer a multiple of 16 bytes, its row stride a multiple
+ *     of 8 elements and at least its columns). A call that finds less than it
+ *     needs says how much that is. A workspace serves any smaller number of
+ *     tokens.
+ *   - Waits: the kernels wait inside, between their own warps. Every wait is
+ *     bounded; one that ran out leaves the call's results undefined and shows
+ *     in fsdp_operators_status.
+ *   - Sizes below 2^31 - 2^9; a call enqueues up to 3 * steps + 2 kernels
+ *     (orthogonalisation) or up to 10 (the others), and clears outputs that are
+ *     sums over nothing with memory-set nodes. */
+
+enum fsdp_activation {
+  FSDP_SILU = 0, /* z / (1 + exp(-z)) */
+  FSDP_GELU = 1, /* z (1 + erf(z / sqrt(2))) / 2 */
+  FSDP_RELU = 2  /* max(z, 0), derivative 0 at 0 */
+};
+
+/* *status = 1 when a wait inside one of these operators' kernels on the current
+ * device has run out since the last question, else 0. Synchronises `stream`. */
+int fsdp_operators_status(fsdp_stream_t stream, int* status);
+
+/* Scratch bytes of fsdp_gated_ffn for that many tokens or fewer; aligned != 0:
+ * for operands whose rows are all on the 16-byte grid. */
+int fsdp_gated_ffn_workspace(int64_t tokens, int64_t hidden, int64_t inner, int aligned, size_t* bytes);
+
+/* Gated feed-forward block: with x (tokens x hidden), w_gate and w_up (inner x
+ * hidden) and w_down (hidden x inner),
+ *   g = x w_gate^T,  u = x w_up^T,  h = act(g) * u,  out = h w_down^T.
+ * h is formed from the binary32 sums g and u and rounded to bfloat16 for the
+ * last product. gate and up, both or neither NULL, receive g and u, which the
+ * gradient needs. out, gate and up overlap no other operand. */
+int fsdp_gated_ffn(int64_t tokens, int64_t hidden, int64_t inner, const void* x, int64_t x_stride, const void* w_gate,
+                   int64_t w_gate_stride, const void* w_up, int64_t w_up_stride, const void* w_down,
+                   int64_t w_down_stride, int activation, void* gate, int64_t gate_stride, void* up,
+                   int64_t up_stride, void* out, int64_t out_stride, void* workspace, size_t workspace_bytes,
+                   fsdp_stream_t stream);
+
+/* Scratch bytes of fsdp_gated_ffn_grad, as above. */
+int fsdp_gated_ffn_grad_workspace(int64_t tokens, int64_t hidden, int64_t inner, int aligned, size_t* bytes);
+
+/* Gradient of fsdp_gated_ffn from the gate and up that it gave (any bfloat16
+ * values g, u): with d = grad_out w_down, dg = d * u * act'(g), du = d * act(g)
+ * and h = act(g) * u, each rounded to bfloat16,
+ *   grad_x = dg w_gate + du w_up,    grad_w_gate = dg^T x,
+ *   grad_w_up = du^T x,              grad_w_down = grad_out^T h.
+ * The weights' gradients have type param_grad_dt; with accumulate != 0 they are
+ * added, in binary32, to what is there and rounded once. No output overlaps
+ * another operand. */
+int fsdp_gated_ffn_grad(int64_t tokens, int64_t hidden, int64_t inner, const void* grad_out, int64_t grad_out_stride,
+                        const void* x, int64_t x_stride, const void* w_gate, int64_t w_gate_stride, const void* w_up,
+                        int64_t w_up_stride, const void* w_down, int64_t w_down_stride, const void* gate,
+                        int64_t gate_stride, const void* up, int64_t up_stride, int activation, void* grad_x,
+                        int64_t grad_x_stride, int param_grad_dt, int accumulate, void* grad_w_gate,
+                        int64_t grad_w_gate_stride, void* grad_w_up, int64_t grad_w_up_stride, void* grad_w_down,
+                        int64_t grad_w_down_stride, void* workspace, size_t workspace_bytes, fsdp_stream_t stream);
+
+/* Scratch bytes of fsdp_orthogonalize. */
+int fsdp_orthogonalize_workspace(int64_t rows, int64_t cols, size_t* bytes);
+
+/* Orthogonalises an update, as an optimizer of matrices does before it applies
+ * it: X_0 = x / (|x|_F + eps), then `steps` times, with A = X X^T (X^T X from
+ * the right where rows > cols, which is the same),
+ *   X <- a X + (b A + c A A) X,
+ * and out = scale * X. With the coefficients (3.4445, -4.7750, 2.0315) five
+ * steps bring x's larger singular values to between about 0.7 and 1.2. x has
+ * type dt, out is bfloat16. Inside, X is held in 22 bits and A and the
+ * polynomial in binary16 under a power of two: out is off by about half a step
+ * of bfloat16 more than its own rounding. A sum of the squares of x that
+ * binary32 does not hold is no limit; x with infinities or NaN gives NaN; x = 0
+ * gives 0 for eps > 0. 1 <= steps <= 64; |a|, |b|, |c| <= 256; eps >= 0. */
+int fsdp_orthogonalize(int64_t rows, int64_t cols, int dt, const void* x, int64_t x_stride, int steps, double a,
+                       double b, double c, double scale, double eps, void* out, int64_t out_stride, void* workspace,
+                       size_t workspace_bytes, fsdp_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
