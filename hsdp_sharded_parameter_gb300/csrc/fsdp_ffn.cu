@@ -40,29 +40,39 @@ __device__ __forceinline__ void put_bf16(const Mat& m, int64_t row, int64_t col,
     store_granule(at(m, row, col), r, n);
 }
 
-// out = D, or out + D.
+// out = D, or out + D; each of a group's products has an out of its own.
 template <typename T>
 struct Store {
-    Mat out;
+    static constexpr bool kMirror = false;
+    struct Before {
+        Raw<T> old;
+    };
+    Mat out[kMaxGroup];
     int accumulate;
-    __device__ __forceinline__ void operator()(int64_t row, int64_t col, int n, const Cols& v, const Cols&) const {
-        T* p = static_cast<T*>(out.data) + row * out.stride + col;
+    __device__ __forceinline__ T* place(int i, int64_t row, int64_t col) const {
+        const Mat& o = i == 0 ? out[0] : (i == 1 ? out[1] : out[2]);
+        return static_cast<T*>(o.data) + row * o.stride + col;
+    }
+    __device__ __forceinline__ void bring(int i, int64_t row, int64_t col, int n, Before& b) const {
+        if (accumulate) load_granule(b.old, place(i, row, col), 0, n);
+    }
+    __device__ __forceinline__ void operator()(int i, int, int64_t row, int64_t col, int n, const Cols& v, const Cols&, const Before& b,
+                                               Raw<uint16_t>&) const {
         Raw<T> r;
-        Cols sum = v;
-        if (accumulate) {
-            load_granule(r, p, 0, n);
-            sum = sum + widened(r);
-        }
-        round_to(sum, r);
-        store_granule(p, r, n);
+        round_to(accumulate ? v + widened(b.old) : v, r);
+        store_granule(place(i, row, col), r, n);
     }
 };
 
 // h = act(gate) * up from the two projections, which are kept on request.
 struct Gated {
+    static constexpr bool kMirror = false;
+    struct Before {};
     Mat h, gate, up;
     int act;
-    __device__ __forceinline__ void operator()(int64_t row, int64_t col, int n, const Cols& g, const Cols& u) const {
+    __device__ __forceinline__ void bring(int, int64_t, int64_t, int, Before&) const {}
+    __device__ __forceinline__ void operator()(int, int, int64_t row, int64_t col, int n, const Cols& g, const Cols& u, const Before&,
+                                               Raw<uint16_t>&) const {
         Cols v;
 #pragma unroll
         for (int e = 0; e < 8; ++e) v.set(e, act_value(act, g.get(e)) * u.get(e));
@@ -76,14 +86,19 @@ struct Gated {
 
 // From the gradient d of h: those of gate and up, and h again.
 struct GatedGrad {
+    static constexpr bool kMirror = false;
+    struct Before {
+        Raw<uint16_t> gate, up;
+    };
     Mat gate, up, grad_gate, grad_up, h;
     int act;
-    __device__ __forceinline__ void operator()(int64_t row, int64_t col, int n, const Cols& d, const Cols&) const {
-        Raw<uint16_t> r;
-        load_granule(r, at(gate, row, col), 0, n);
-        const Cols g = widened(r);
-        load_granule(r, at(up, row, col), 0, n);
-        const Cols u = widened(r);
+    __device__ __forceinline__ void bring(int, int64_t row, int64_t col, int n, Before& b) const {
+        load_granule(b.gate, at(gate, row, col), 0, n);
+        load_granule(b.up, at(up, row, col), 0, n);
+    }
+    __device__ __forceinline__ void operator()(int, int, int64_t row, int64_t col, int n, const Cols& d, const Cols&, const Before& b,
+                                               Raw<uint16_t>&) const {
+        const Cols g = widened(b.gate), u = widened(b.up);
         Cols dg, du, v;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -99,41 +114,98 @@ struct GatedGrad {
     }
 };
 
-int64_t padded(int64_t n) { return (n + 7) / 8 * 8; }
-size_t room(int64_t rows, int64_t cols) { return (size_t)((rows * padded(cols) * 2 + 255) / 256 * 256); }
+// ------------------------------------------------------------ the products
+
+Product gated_product(const FfnArgs& a) {
+    return {a.tokens, a.inner, 1, {a.hidden, 0}, {a.x, {}}, {a.w_gate, a.w_up}, 0, 0, 0, 1, 0};
+}
+Product out_product(const FfnArgs& a, const Mat& h) {
+    return {a.tokens, a.hidden, 1, {a.inner, 0}, {h, {}}, {a.w_down, {}}, 0, 0, 0, 0, 0};
+}
+Product through_product(const FfnGradArgs& a) {
+    return {a.tokens, a.inner, 1, {a.hidden, 0}, {a.grad, {}}, {a.w_down, {}}, 0, 1, 0, 0, 0};
+}
+Product x_product(const FfnGradArgs& a, const Mat& dg, const Mat& du) {
+    return {a.tokens, a.hidden, 2, {a.inner, a.inner}, {dg, du}, {a.w_gate, a.w_up}, 0, 1, 0, 0, 0};
+}
+
+// Room for the parts' sums of the larger of two products.
+size_t sums_room(size_t a, size_t b) { return (std::max(a, b) + 255) / 256 * 256; }
+size_t copy_room(const Mat& f, int64_t rows, int64_t cols) { return copies_read(f, rows, cols) ? 0 : aligned_room(rows, cols); }
 
 }  // namespace
 
-size_t ffn_bytes(const FfnArgs& a) { return room(a.tokens, a.inner); }
-size_t ffn_grad_bytes(const FfnGradArgs& a) { return 3 * room(a.tokens, a.inner); }
-size_t ffn_most_bytes(int64_t tokens, int64_t, int64_t inner, bool) { return room(tokens, inner); }
-size_t ffn_grad_most_bytes(int64_t tokens, int64_t, int64_t inner, bool) { return 3 * room(tokens, inner); }
+size_t ffn_bytes(const FfnArgs& a) {
+    return aligned_room(a.tokens, a.inner) + sums_room(parts_bytes(gated_product(a)), parts_bytes(out_product(a, {}))) +
+           copy_room(a.x, a.tokens, a.hidden) + copy_room(a.w_gate, a.inner, a.hidden) + copy_room(a.w_up, a.inner, a.hidden) +
+           copy_room(a.w_down, a.hidden, a.inner);
+}
+size_t ffn_most_bytes(int64_t tokens, int64_t hidden, int64_t inner, bool aligned) {
+    const size_t copies = aligned ? 0 : aligned_room(tokens, hidden) + 2 * aligned_room(inner, hidden) + aligned_room(hidden, inner);
+    return aligned_room(tokens, inner) + sums_room(parts_most_bytes(tokens, inner, 2), parts_most_bytes(tokens, hidden, 1)) + copies;
+}
+size_t ffn_grad_bytes(const FfnGradArgs& a) {
+    return 3 * aligned_room(a.tokens, a.inner) + sums_room(parts_bytes(through_product(a)), parts_bytes(x_product(a, {}, {}))) +
+           copy_room(a.grad, a.tokens, a.hidden) + copy_room(a.x, a.tokens, a.hidden) + copy_room(a.w_gate, a.inner, a.hidden) +
+           copy_room(a.w_up, a.inner, a.hidden) + copy_room(a.w_down, a.hidden, a.inner);
+}
+size_t ffn_grad_most_bytes(int64_t tokens, int64_t hidden, int64_t inner, bool aligned) {
+    const size_t copies = aligned ? 0 : 2 * aligned_room(tokens, hidden) + 2 * aligned_room(inner, hidden) + aligned_room(hidden, inner);
+    return 3 * aligned_room(tokens, inner) + sums_room(parts_most_bytes(tokens, inner, 1), parts_most_bytes(tokens, hidden, 1)) + copies;
+}
 
-cudaError_t launch_ffn(const FfnArgs& a, cudaStream_t s) {
-    const Mat h = {a.work, padded(a.inner)};
-    const Product in = {a.tokens, a.inner, 1, {a.hidden, 0}, {a.x, {}}, {a.w_gate, a.w_up}, 0, 0, 0, 1};
-    const Product out = {a.tokens, a.hidden, 1, {a.inner, 0}, {h, {}}, {a.w_down, {}}, 0, 0, 0, 0};
-    cudaError_t e = launch_product(in, Gated{h, a.gate, a.up, a.act}, s, true);
-    if (e == cudaSuccess) e = launch_product(out, Store<uint16_t>{a.out, 0}, s, false);
+cudaError_t launch_ffn(const FfnArgs& args, cudaStream_t s) {
+    FfnArgs a = args;
+    Copies c = {};
+    char* room = a.work;
+    const Mat h = {room, whole_granules(a.inner)};
+    room += aligned_room(a.tokens, a.inner);
+    float* sums = reinterpret_cast<float*>(room);
+    room += sums_room(parts_bytes(gated_product(a)), parts_bytes(out_product(a, h)));
+    a.x = readable(a.x, a.tokens, a.hidden, &c, &room);
+    a.w_gate = readable(a.w_gate, a.inner, a.hidden, &c, &room);
+    a.w_up = readable(a.w_up, a.inner, a.hidden, &c, &room);
+    a.w_down = readable(a.w_down, a.hidden, a.inner, &c, &room);
+    if (a.tokens == 0) return cudaSuccess;
+    cudaError_t e = launch_copies(c, s);
+    if (e == cudaSuccess) e = launch_product(gated_product(a), Gated{h, a.gate, a.up, a.act}, sums, s, c.n == 0);
+    if (e == cudaSuccess) e = launch_product(out_product(a, h), Store<uint16_t>{{a.out, {}, {}}, 0}, sums, s, false);
     return e;
 }
 
 namespace {
 template <typename T>
-cudaError_t ffn_grad(const FfnGradArgs& a, cudaStream_t s) {
-    const size_t each = room(a.tokens, a.inner);
-    const int64_t ld = padded(a.inner);
-    const Mat dg = {a.work, ld}, du = {a.work + each, ld}, h = {a.work + 2 * each, ld};
-    const Product through = {a.tokens, a.inner, 1, {a.hidden, 0}, {a.grad, {}}, {a.w_down, {}}, 0, 1, 0, 0};
-    const Product dx = {a.tokens, a.hidden, 2, {a.inner, a.inner}, {dg, du}, {a.w_gate, a.w_up}, 0, 1, 0, 0};
-    const Product down = {a.hidden, a.inner, 1, {a.tokens, 0}, {a.grad, {}}, {h, {}}, 1, 1, 0, 0};
-    Product side = {a.inner, a.hidden, 1, {a.tokens, 0}, {dg, {}}, {a.x, {}}, 1, 1, 0, 0};
-    cudaError_t e = launch_product(through, GatedGrad{a.gate, a.up, dg, du, h, a.act}, s, true);
-    if (e == cudaSuccess) e = launch_product(dx, Store<uint16_t>{a.grad_x, 0}, s, false);
-    if (e == cudaSuccess) e = launch_product(down, Store<T>{a.grad_down, a.accumulate}, s, false);
-    if (e == cudaSuccess) e = launch_product(side, Store<T>{a.grad_gate, a.accumulate}, s, false);
-    side.a[0] = du;
-    if (e == cudaSuccess) e = launch_product(side, Store<T>{a.grad_up, a.accumulate}, s, false);
+cudaError_t ffn_grad(const FfnGradArgs& args, cudaStream_t s) {
+    FfnGradArgs a = args;
+    Copies c = {};
+    char* room = a.work;
+    const size_t each = aligned_room(a.tokens, a.inner);
+    const int64_t ld = whole_granules(a.inner);
+    const Mat dg = {room, ld}, du = {room + each, ld}, h = {room + 2 * each, ld};
+    room += 3 * each;
+    float* sums = reinterpret_cast<float*>(room);
+    room += sums_room(parts_bytes(through_product(a)), parts_bytes(x_product(a, dg, du)));
+    a.grad = readable(a.grad, a.tokens, a.hidden, &c, &room);
+    a.x = readable(a.x, a.tokens, a.hidden, &c, &room);
+    a.w_gate = readable(a.w_gate, a.inner, a.hidden, &c, &room);
+    a.w_up = readable(a.w_up, a.inner, a.hidden, &c, &room);
+    a.w_down = readable(a.w_down, a.hidden, a.inner, &c, &room);
+    const Product weights[3] = {{a.inner, a.hidden, 1, {a.tokens, 0}, {dg, {}}, {a.x, {}}, 1, 1, 0, 0, 0},
+                                {a.inner, a.hidden, 1, {a.tokens, 0}, {du, {}}, {a.x, {}}, 1, 1, 0, 0, 0},
+                                {a.hidden, a.inner, 1, {a.tokens, 0}, {a.grad, {}}, {h, {}}, 1, 1, 0, 0, 0}};
+    const Store<T> store = {{a.grad_gate, a.grad_up, a.grad_down}, a.accumulate};
+    if (a.tokens == 0) {
+        // sums over nothing
+        for (int i = 0; i < 3; ++i) {
+            const cudaError_t e = launch_product(weights[i], Store<T>{{store.out[i], {}, {}}, a.accumulate}, nullptr, s, true);
+            if (e != cudaSuccess) return e;
+        }
+        return cudaSuccess;
+    }
+    cudaError_t e = launch_copies(c, s);
+    if (e == cudaSuccess) e = launch_product(through_product(a), GatedGrad{a.gate, a.up, dg, du, h, a.act}, sums, s, c.n == 0);
+    if (e == cudaSuccess) e = launch_product(x_product(a, dg, du), Store<uint16_t>{{a.grad_x, {}, {}}, 0}, sums, s, false);
+    if (e == cudaSuccess && a.inner > 0 && a.hidden > 0) e = launch_group(weights, 3, store, cut_of(weights[0], false), s, false);
     return e;
 }
 }  // namespace

@@ -279,38 +279,55 @@ __global__ void __launch_bounds__(kNarrowThreads) narrow_apply_kernel(Mat x, int
 
 // A = X X^T.
 struct Gram {
+    static constexpr bool kMirror = true;
+    struct Before {};
     Mat out;
     float scale;
-    __device__ __forceinline__ void operator()(int64_t row, int64_t col, int n, const Cols& v, const Cols&) const {
-        put_half(out, row, col, n, v * all(scale));
+    __device__ __forceinline__ void bring(int, int64_t, int64_t, int, Before&) const {}
+    __device__ __forceinline__ void put(int64_t row, int64_t col, int n, const Raw<uint16_t>& r) const { store_granule(at(out, row, col), r, n); }
+    __device__ __forceinline__ void operator()(int, int, int64_t row, int64_t col, int n, const Cols& v, const Cols&, const Before&,
+                                               Raw<uint16_t>& r) const {
+        round_half(v * all(scale), r);
+        put(row, col, n, r);
     }
 };
 
 // c A A + b A + d I.
 struct Poly {
+    static constexpr bool kMirror = true;
+    struct Before {
+        Raw<uint16_t> a;
+    };
     Mat a, out;
     float square, linear, diagonal;
-    __device__ __forceinline__ void operator()(int64_t row, int64_t col, int n, const Cols& v, const Cols&) const {
-        Raw<uint16_t> r;
-        load_granule(r, at(a, row, col), 0, n);
-        Cols s = fma(v, all(square), widened_half(r) * all(linear));
+    __device__ __forceinline__ void bring(int, int64_t row, int64_t col, int n, Before& b) const { load_granule(b.a, at(a, row, col), 0, n); }
+    __device__ __forceinline__ void put(int64_t row, int64_t col, int n, const Raw<uint16_t>& r) const { store_granule(at(out, row, col), r, n); }
+    __device__ __forceinline__ void operator()(int, int, int64_t row, int64_t col, int n, const Cols& v, const Cols&, const Before& b,
+                                               Raw<uint16_t>& r) const {
+        Cols s = fma(v, all(square), widened_half(b.a) * all(linear));
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             if (col + e == row) s.set(e, s.get(e) + diagonal);
-        put_half(out, row, col, n, s);
+        round_half(s, r);
+        put(row, col, n, r);
     }
 };
 
 // X <- shift X + D, into the planes, or at the end into the caller's matrix.
 struct Next {
+    static constexpr bool kMirror = false;
+    struct Before {
+        Raw<uint16_t> hi, lo;
+    };
     Mat hi, lo, next, out;  // out.data: the caller's
     float scale, shift;
-    __device__ __forceinline__ void operator()(int64_t row, int64_t col, int n, const Cols& v, const Cols&) const {
-        Raw<uint16_t> r;
-        load_granule(r, at(hi, row, col), 0, n);
-        Cols x = widened_half(r);
-        load_granule(r, at(lo, row, col), 0, n);
-        x = fma(widened_half(r), all(1.0f / kLow), x);
+    __device__ __forceinline__ void bring(int, int64_t row, int64_t col, int n, Before& b) const {
+        load_granule(b.hi, at(hi, row, col), 0, n);
+        load_granule(b.lo, at(lo, row, col), 0, n);
+    }
+    __device__ __forceinline__ void operator()(int, int, int64_t row, int64_t col, int n, const Cols& v, const Cols&, const Before& b,
+                                               Raw<uint16_t>& r) const {
+        Cols x = fma(widened_half(b.lo), all(1.0f / kLow), widened_half(b.hi));
         x = fma(v, all(scale), x * all(shift));
         if (!out.data) {
             put_planes(next, lo, row, col, n, x);
@@ -321,8 +338,6 @@ struct Next {
     }
 };
 
-int64_t padded(int64_t n) { return (n + 7) / 8 * 8; }
-size_t room(int64_t rows, int64_t cols) { return (size_t)((rows * padded(cols) * 2 + 255) / 256 * 256); }
 constexpr size_t kPartsRoom = (3 * kSquareBlocks * 4 + 255) / 256 * 256;
 
 constexpr size_t kNarrowRoom = (size_t)(kGramBlocks + 1) * kSide * kSide * 4;
@@ -353,25 +368,42 @@ cudaError_t narrow(const OrthoArgs& a, cudaStream_t s) {
 
 int log2_near(double v) { return (int)std::nearbyint(std::log2(v)); }
 
+// The products of a step; which factor's rows are neighbours in memory goes by
+// the longer side.
+Product gram_product(int64_t p, int64_t q, int tall, const Mat& x) {
+    return {p, p, 1, {q, 0}, {x, {}}, {x, {}}, tall, tall, 1, 0, 1};
+}
+Product square_product(int64_t p, const Mat& a) { return {p, p, 1, {p, 0}, {a, {}}, {a, {}}, 0, 0, 1, 0, 1}; }
+Product next_product(int64_t rows, int64_t cols, const Mat& poly, const Mat& x) {
+    if (rows > cols) return {rows, cols, 1, {cols, 0}, {x, {}}, {poly, {}}, 0, 0, 1, 0, 0};
+    return {rows, cols, 1, {rows, 0}, {poly, {}}, {x, {}}, 0, 1, 1, 0, 0};
+}
+size_t sums_bytes(int64_t rows, int64_t cols) {
+    const int64_t p = std::min(rows, cols), q = std::max(rows, cols);
+    const size_t most = std::max({parts_bytes(gram_product(p, q, 0, {})), parts_bytes(square_product(p, {})), parts_bytes(next_product(rows, cols, {}, {}))});
+    return (most + 255) / 256 * 256;
+}
+
 }  // namespace
 
 size_t ortho_bytes(int64_t rows, int64_t cols) {
     if (rows == 0 || cols == 0) return 0;
     const int64_t p = rows < cols ? rows : cols;
     if (p <= kSide) return kPartsRoom + kNarrowRoom;
-    return kPartsRoom + 3 * room(rows, cols) + 2 * room(p, p);
+    return kPartsRoom + 3 * aligned_room(rows, cols) + 2 * aligned_room(p, p) + sums_bytes(rows, cols);
 }
 
 cudaError_t launch_ortho(int dt, const OrthoArgs& a, cudaStream_t s) {
     if (a.rows == 0 || a.cols == 0) return cudaSuccess;
     const bool tall = a.rows > a.cols;
     const int64_t p = tall ? a.cols : a.rows, q = tall ? a.rows : a.cols;
-    const size_t plane = room(a.rows, a.cols);
-    const int64_t ld = padded(a.cols), lp = padded(p);
+    const size_t plane = aligned_room(a.rows, a.cols);
+    const int64_t ld = whole_granules(a.cols), lp = whole_granules(p);
     float* parts = reinterpret_cast<float*>(a.work);
     char* w = a.work + kPartsRoom;
     Mat hi = {w, ld}, next = {w + plane, ld};
-    const Mat lo = {w + 2 * plane, ld}, gram = {w + 3 * plane, lp}, poly = {w + 3 * plane + room(p, p), lp};
+    const Mat lo = {w + 2 * plane, ld}, gram = {w + 3 * plane, lp}, poly = {w + 3 * plane + aligned_room(p, p), lp};
+    float* sums = reinterpret_cast<float*>(w + 3 * plane + 2 * aligned_room(p, p));
     // Scales by powers of two that keep values in binary16's normal range: X's
     // elements are about 1/sqrt(p q) at first and 1/sqrt(q) at the end, never
     // above about 1.2; A's diagonal about 1/p at first; the polynomial's at most
@@ -396,21 +428,14 @@ cudaError_t launch_ortho(int dt, const OrthoArgs& a, cudaStream_t s) {
     count_launch();
     for (int i = 0; i < a.steps && e == cudaSuccess; ++i) {
         const float shift = i + 2 < a.steps ? a.a : 0.5f * (1.0f + a.a);
-        const Product square = {p, p, 1, {q, 0}, {hi, {}}, {hi, {}}, tall, tall, 1, 0};
-        e = launch_product(square, Gram{gram, std::ldexp(1.0f, sa - 2 * sx)}, s, false);
-        const Product again = {p, p, 1, {p, 0}, {gram, {}}, {gram, {}}, 0, 0, 1, 0};
+        e = launch_product(gram_product(p, q, tall, hi), Gram{gram, std::ldexp(1.0f, sa - 2 * sx)}, sums, s, false);
         const Poly mix = {gram, poly, std::ldexp(a.c, sb - 2 * sa), std::ldexp(a.b, sb - sa), std::ldexp(a.a - shift, sb)};
-        if (e == cudaSuccess) e = launch_product(again, mix, s, false);
-        Product apply = {a.rows, a.cols, 1, {p, 0}, {poly, {}}, {hi, {}}, 0, 1, 1, 0};
-        if (tall) {
-            apply.a[0] = hi;
-            apply.b[0] = poly;
-            apply.b_mn = 0;
-        }
+        if (e == cudaSuccess) e = launch_product(square_product(p, gram), mix, sums, s, false);
         const bool last = i + 1 == a.steps;
         const float out = last ? std::ldexp(a.scale, -sx) : 1.0f;
         if (e == cudaSuccess)
-            e = launch_product(apply, Next{hi, lo, next, last ? a.out : Mat{nullptr, 0}, std::ldexp(out, -sb), shift * out}, s, false);
+            e = launch_product(next_product(a.rows, a.cols, poly, hi),
+                               Next{hi, lo, next, last ? a.out : Mat{nullptr, 0}, std::ldexp(out, -sb), shift * out}, sums, s, false);
         std::swap(hi, next);
     }
     return e;
