@@ -73,11 +73,13 @@ __device__ __forceinline__ uint64_t clock_ns() {
 __device__ int gave_up;
 constexpr uint64_t kWaitNs = 2000000000ull;
 // Waits for the phase of a parity: false, and said so, once two seconds have
-// passed.
+// passed. (The clock is read seldom: a read takes longer than a step of the
+// products, and the wait does not see its phase end meanwhile.)
 __device__ __noinline__ bool bar_wait_long(uint64_t* b, uint32_t parity) {
     const uint64_t from = clock_ns();
-    for (uint32_t i = 0; i < (1u << 26); ++i) {
-        if (bar_test(b, parity)) return true;
+    for (uint32_t i = 0; i < (1u << 20); ++i) {
+        for (int k = 0; k < 256; ++k)
+            if (bar_test(b, parity)) return true;
         if (clock_ns() - from > kWaitNs) break;
     }
     atomicOr(&gave_up, 1);
@@ -85,7 +87,7 @@ __device__ __noinline__ bool bar_wait_long(uint64_t* b, uint32_t parity) {
 }
 __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity) {
 #pragma unroll 1
-    for (int i = 0; i < 64; ++i)
+    for (int i = 0; i < 1024; ++i)
         if (bar_test(b, parity)) return true;
     return bar_wait_long(b, parity);
 }
@@ -102,6 +104,15 @@ __device__ __forceinline__ void bar_expect(uint64_t* b, uint32_t bytes) {
 }
 __device__ __forceinline__ void cluster_meet() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// One lane of a warp, which the compiler knows to be one: the operands of the
+// copies and of the tensor cores' instructions are a warp's, and behind a
+// comparison of lanes each is brought there by a loop over the lanes.
+__device__ __forceinline__ bool one_lane() {
+    uint32_t one;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(one));
+    return one != 0;
 }
 
 // --------------------------------------------------- tensor core instructions
@@ -230,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     __shared__ uint32_t tmem_at;
     char* base = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
     float* stages = reinterpret_cast<float*>(base + kStg * kBytes);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = __shfl_sync(kFull, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     uint32_t rank;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     if (threadIdx.x == 0) {
@@ -258,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     const int tiles = t.first[t.group], items = tiles * t.splits, steps = t.steps[0] + t.steps[1];
     const int pairs = gridDim.x / 2, pair = blockIdx.x / 2;
     if (warp == 0) {
-        if (lane == 0) {
+        if (one_lane()) {
             // brings the tiles' rows
             int stage = 0, brought = 0;
             uint32_t phase = 0;
@@ -310,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             }
         }
     } else if (warp == 1) {
-        if (rank == 0 && lane == 0) {
+        if (rank == 0 && one_lane()) {
             // issues the products
             int stage = 0, n_done = 0;
             uint32_t phase = 0;
