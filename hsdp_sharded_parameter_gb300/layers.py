@@ -1,4 +1,4 @@
-"""A trainable block on one HSDP unit, built from the training operators.
+"""Trainable blocks on one HSDP unit, built from the training operators.
 
 ``TokenBlock`` is the input end of a pre-norm transformer with one sublayer,
 for all rank_size virtual ranks of a plan. Its parameters are sharded with the
@@ -104,6 +104,78 @@ class TokenBlock:
         """Plain gradient descent on the shards."""
         for shard, grad in zip(self.unit.shards, self.unit.shard_grads):
             shard.add_(grad, alpha=-lr)
+
+    def close(self):
+        self.unit.close()
+        self.plan.close()
+
+
+class GatedBlock:
+    """The gated feed-forward block of a layer on one HSDP unit, with the
+    optimizer step of its matrices: forward fsdp_gated_ffn on the gathered
+    parameters, backward fsdp_gated_ffn_grad into the unit's gradients and
+    their reduction, and an update by momentum that fsdp_orthogonalize makes
+    orthogonal, of which every rank applies its own rows. The ranks live on one
+    GPU, so each matrix's update is computed once."""
+
+    def __init__(self, hidden, inner, tokens, rank_size, shard_size, activation="silu", device="cuda"):
+        self.hidden, self.inner, self.activation = hidden, inner, activation
+        # w_gate, w_up, w_down
+        self.shapes = [(inner, hidden), (inner, hidden), (hidden, inner)]
+        self.plan = C.Plan([s[0] for s in self.shapes], [s[1] for s in self.shapes], rank_size, shard_size).upload()
+        self.unit = HsdpUnit(self.plan, "bf16", "bf16", device=device)
+        new = lambda *s, dtype=torch.bfloat16: torch.empty(*s, dtype=dtype, device=device)  # noqa: E731
+        W = self.plan.W
+        self.gate, self.up = ([new(tokens, inner) for _ in range(W)] for _ in range(2))
+        self.out, self.grad_x = ([new(tokens, hidden) for _ in range(W)] for _ in range(2))
+        self.momentum = [torch.zeros(s, dtype=torch.float32, device=device) for s in self.shapes]
+        most = max(C.fsdp_gated_ffn_workspace(tokens, hidden, inner, aligned=False),
+                   C.fsdp_gated_ffn_grad_workspace(tokens, hidden, inner, aligned=False),
+                   C.fsdp_orthogonalize_workspace(inner, hidden), C.fsdp_orthogonalize_workspace(hidden, inner))
+        self.work = new(most, dtype=torch.uint8)
+
+    def init_parameters(self, seed=0, std=0.02):
+        """The same N(0, std^2) values on every replica."""
+        gen = torch.Generator(device=self.unit.device)
+        gen.manual_seed(seed)
+        for q, shape in enumerate(self.shapes):
+            full = torch.randn(shape, generator=gen, device=self.unit.device) * std
+            for w in range(self.plan.W):
+                first, n = self.plan.sharded_size(q, w % self.plan.S)
+                self.unit.shards[w * self.plan.P + q].copy_(full[first:first + n].reshape(-1))
+
+    def _views(self, tensors, w):
+        return [t.view(s) for t, s in zip(tensors[w * self.plan.P:(w + 1) * self.plan.P], self.shapes)]
+
+    def forward(self, x):
+        """x[w]: rank w's bfloat16 tokens. Returns out[w]."""
+        self.unit.unshard_direct()
+        for w in range(self.plan.W):
+            C.fsdp_gated_ffn(x[w], *self._views(self.unit.full, w), self.out[w], self.work, self.activation, self.gate[w], self.up[w])
+        return self.out
+
+    def backward(self, x, grad_out, op="avg"):
+        """grad_out[w]: the gradient of out[w]. Fills the unit's gradients,
+        reduces them over the mesh and returns grad_x[w]."""
+        for w in range(self.plan.W):
+            C.fsdp_gated_ffn_grad(grad_out[w], x[w], *self._views(self.unit.full, w), self.gate[w], self.up[w], self.grad_x[w],
+                                  *self._views(self.unit.grads, w), self.work, self.activation)
+        self.unit.reduce_grads_one_pass(op)
+        return self.grad_x
+
+    def step(self, lr, mu=0.95):
+        """Momentum, orthogonalised, onto the shards: scaled by
+        sqrt(max(1, rows / cols))."""
+        for q, (rows, cols) in enumerate(self.shapes):
+            m = self.momentum[q].mul_(mu)
+            spans = [self.plan.sharded_size(q, s) for s in range(self.plan.S)]
+            for s, (first, n) in enumerate(spans):
+                m[first:first + n].add_(self.unit.shard_grads[s * self.plan.P + q].view(n, cols))
+            update = torch.empty(rows, cols, dtype=torch.bfloat16, device=m.device)
+            C.fsdp_orthogonalize(m, update, self.work, scale=math.sqrt(max(1.0, rows / cols)))
+            for w in range(self.plan.W):
+                first, n = spans[w % self.plan.S]
+                self.unit.shards[w * self.plan.P + q].view(n, cols).add_(update[first:first + n], alpha=-lr)
 
     def close(self):
         self.unit.close()

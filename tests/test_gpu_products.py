@@ -206,3 +206,72 @@ def test_orthogonalize_borders():
         assert bool(torch.isnan(ortho(x)).all())
     for shape in [(0, 5), (5, 0), (0, 0)]:
         ortho(torch.zeros(*shape, device="cuda"))
+
+
+def test_equal_bits_on_other_streams_and_in_graphs():
+    # one graph of the three operators in a row, one workspace
+    b = Block(300, 136, 520)
+    t, h, f = b.sizes
+    new = lambda *s: torch.empty(*s, dtype=BF16, device="cuda")  # noqa: E731
+    y, g, u, dx, d = new(t, h), new(t, f), new(t, f), new(t, h), [torch.empty_like(w) for w in b.w]
+    o = new(f, h)
+    work = torch.empty(max(C.fsdp_gated_ffn_workspace(t, h, f), C.fsdp_gated_ffn_grad_workspace(t, h, f), C.fsdp_orthogonalize_workspace(f, h)),
+                       dtype=torch.uint8, device="cuda")
+
+    def run():
+        C.fsdp_gated_ffn(b.x, *b.w, y, work, "silu", g, u)
+        C.fsdp_gated_ffn_grad(b.grad, b.x, *b.w, g, u, dx, *d, work)
+        C.fsdp_orthogonalize(d[0], o, work)
+
+    run()
+    torch.cuda.synchronize()
+    outs = [y, g, u, dx, *d, o]
+    want = [v.clone() for v in outs]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, v) for a, v in zip(outs, want))
+    with torch.cuda.graph(graph):
+        run()
+    for _ in range(2):
+        for v in outs:
+            v.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, v) for a, v in zip(outs, want))
+
+
+def test_gated_block_on_a_mesh():
+    from hsdp_sharded_parameter_gb300.layers import GatedBlock
+
+    block = GatedBlock(72, 200, 90, 4, 2)
+    block.init_parameters(1, 0.1)
+    x, grad = [rand(10 + w, 90, 72) for w in range(4)], [rand(20 + w, 90, 72, 0.1) for w in range(4)]
+    out = block.forward(x)
+    grad_x = block.backward(x, grad)
+    mean = [0.0, 0.0, 0.0]
+    for w in range(4):
+        p = block._views(block.unit.full, w)
+        R.agree("out", out[w], R.gated_ffn(x[w], *p, "silu")["out"])
+        want = R.gated_ffn_grad(grad[w], x[w], *p, block.gate[w], block.up[w], "silu")
+        R.agree("grad_x", grad_x[w], want["x"])
+        for q, k in enumerate(("w_gate", "w_up", "w_down")):
+            R.agree(k, block._views(block.unit.grads, w)[q], want[k])
+            mean[q] = mean[q] + R.d(block._views(block.unit.grads, w)[q]) / 4
+    before = [t.clone() for t in block.unit.shards]
+    block.step(0.5)
+    for q, (rows, cols) in enumerate(block.shapes):
+        # the reduced gradient is rounded to bfloat16, which the update sees as 2^-8 of its values at most
+        got = torch.cat([block.unit.shard_grads[s * 3 + q].view(-1, cols) for s in range(2)])
+        assert bool(((R.d(got) - mean[q]).abs() <= 2.0 ** -8 * mean[q].abs() + 1e-6).all())
+        update = R.orthogonalize(got, scale=max(1.0, rows / cols) ** 0.5)
+        for w in range(4):
+            first, n = block.plan.sharded_size(q, w % 2)
+            moved = R.d(before[w * 3 + q]).view(n, cols) - R.d(block.unit.shards[w * 3 + q]).view(n, cols)
+            # each value is rounded once more as it is added: by 2^-8 of what it becomes
+            off = (moved - 0.5 * update[first:first + n]).norm()
+            assert float(off) <= ORTHO * 0.5 * float(update.norm()) + 2.0 ** -8 * float(R.d(block.unit.shards[w * 3 + q]).norm())
+    block.close()
