@@ -518,9 +518,8 @@ int fsdp_layer_norm_grad(int64_t rows, int64_t cols, int dt, const void* grad_ou
  *   - Waits: the kernels wait inside, between their own warps. Every wait is
  *     bounded; one that ran out leaves the call's results undefined and shows
  *     in fsdp_operators_status.
- *   - Sizes below 2^31 - 2^9; a call enqueues up to 3 * steps + 2 kernels
- *     (orthogonalisation) or up to 10 (the others), and clears outputs that are
- *     sums over nothing with memory-set nodes. */
+ *   - Sizes below 2^31 - 2^9; a call enqueues up to 6 * steps + 2 kernels
+ *     (orthogonalisation) or up to 6 (the others). */
 
 enum fsdp_activation {
   FSDP_SILU = 0, /* z / (1 + exp(-z)) */
