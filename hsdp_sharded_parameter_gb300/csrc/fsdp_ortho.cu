@@ -136,28 +136,26 @@ __global__ void __launch_bounds__(256) planes_kernel(Mat x, int64_t rows, int64_
 
 // ------------------------------------------------------ one short side
 //
-// With at most 64 rows (or columns) everything after the first A happens in
-// p x p matrices, which are polynomials of A and commute: with M = a I + b A +
-// c A A a step is P <- M P, A <- M M A, and at the end X = P X_0. All of it in
-// binary32, in one block. (So few values average no rounding: in binary16 a
-// 1 x 1 matrix is 0.007 off.)
-constexpr int kSide = 64, kChunk = 64, kSidePitch = kSide + 4, kGramBlocks = 64, kNarrowThreads = 256;
+// With at most 64 rows (or columns) X stays in binary32, in blocks of 64 of its
+// columns (rows, where tall), and every step forms A from it anew: a block of
+// threads multiplies its blocks of columns by a I + b A + c A A and adds up what
+// they are to the next A. (So few values average no rounding: in binary16 a 1 x
+// 1 matrix is 0.007 off. A <- M M A, with M the polynomial, would need no X
+// until the end, but where x has nothing A's eigenvalues are what rounding
+// leaves, of either sign, and that recursion multiplies them by a a a step: 64 x
+// 200 of eight strong directions over 0.1% of noise were off by half after
+// eight steps, and NaN after twelve. X X^T has no negative ones but for one
+// step's rounding.)
+//
+// None of these kernels lets the next one's blocks in early: those would take
+// their places on the SMs that are free first, several to one (64 x 4096, five
+// steps: 85 us, and 151 with that; 64 x 28672 144 and 171; 64 x 200 77 and 145).
+constexpr int kSide = 64, kChunk = 64, kSidePitch = kSide + 4, kGramBlocks = 608, kNarrowThreads = 256;
 constexpr int kSideValues = kSide * kSidePitch;
+constexpr int kNarrowSmem = 3 * kSideValues * 4;
 
 __device__ __forceinline__ float value_of(const float* p) { return *p; }
 __device__ __forceinline__ float value_of(const uint16_t* p) { return bf16_to_f32(*p); }
-
-// kChunk columns of X (rows, where tall) from j0 on, to[j][i].
-template <typename T>
-__device__ __forceinline__ void bring_chunk(float* to, const Mat& x, int tall, int p, int64_t q, int64_t j0, float2 f) {
-    const T* data = static_cast<const T*>(x.data);
-    for (int c = threadIdx.x; c < kSide * kChunk; c += kNarrowThreads) {
-        const int i = tall ? c % kSide : c / kChunk, j = tall ? c / kSide : c % kChunk;
-        float v = 0.0f;
-        if (i < p && j0 + j < q) v = value_of(tall ? data + (j0 + j) * x.stride + i : data + i * x.stride + j0 + j) * f.x * f.y;
-        to[j * kSidePitch + i] = v;
-    }
-}
 
 // A thread's 4 x 4 values of sum over k of a[k][i] b[k][j].
 __device__ __forceinline__ void small_product(float (&s)[4][4], const float* a, const float* b, int k_end, int i0, int j0) {
@@ -172,107 +170,116 @@ __device__ __forceinline__ void small_product(float (&s)[4][4], const float* a, 
     }
 }
 
-// A block's share of A = X X^T.
-template <typename T>
-__global__ void __launch_bounds__(kNarrowThreads) narrow_gram_kernel(Mat x, int tall, int p, int64_t q, const float* parts, double eps,
-                                                                     float* grams) {
-    __shared__ __align__(16) float chunk[kChunk * kSidePitch];
-    wait_for_previous();
-    const float2 f = norm_factor(parts, eps, 1.0f);
-    const int i0 = threadIdx.x / 16 * 4, j0 = threadIdx.x % 16 * 4;
-    float s[4][4] = {};
-    for (int64_t j = (int64_t)blockIdx.x * kChunk; j < q; j += (int64_t)gridDim.x * kChunk) {
-        bring_chunk<T>(chunk, x, tall, p, q, j, f);
-        __syncthreads();
-        if (i0 < p && j0 < p) small_product(s, chunk, chunk, kChunk, i0, j0);
-        __syncthreads();
+// A thread's 4 x 4 values of a block's share of A.
+struct GramShare {
+    float s[4][4];
+    __device__ __forceinline__ GramShare() : s{} {}
+    __device__ __forceinline__ void add(const float* columns, int p, int i0, int j0) {
+        if (i0 < p && j0 < p) small_product(s, columns, columns, kChunk, i0, j0);
     }
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-        *reinterpret_cast<float4*>(grams + ((int64_t)blockIdx.x * kSide + i0 + r) * kSide + j0) = make_float4(s[r][0], s[r][1], s[r][2], s[r][3]);
-}
-
-// The steps on A, from its parts; P times scale to `poly`.
-__global__ void __launch_bounds__(kNarrowThreads) narrow_steps_kernel(const float* grams, int n_parts, int p, int steps, float a, float b, float c,
-                                                                      float scale, float* poly) {
-    extern __shared__ __align__(16) float box[];
-    float *A = box, *M = box + kSideValues, *P = box + 2 * kSideValues, *S = box + 3 * kSideValues;
-    wait_for_previous();
-    for (int e = threadIdx.x; e < kSide * kSide; e += kNarrowThreads) {
-        float sum = 0.0f;
-        for (int k = 0; k < n_parts; ++k) sum += grams[(int64_t)k * kSide * kSide + e];
-        A[e / kSide * kSidePitch + e % kSide] = sum;
-        P[e / kSide * kSidePitch + e % kSide] = e / kSide == e % kSide ? 1.0f : 0.0f;
-    }
-    __syncthreads();
-    const int i0 = threadIdx.x / 16 * 4, j0 = threadIdx.x % 16 * 4, k_end = (p + 3) / 4 * 4;
-    const bool in = i0 < p && j0 < p;
-    auto keep = [&](float* to, const float (&s)[4][4]) {
-        if (!in) return;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) *reinterpret_cast<float4*>(to + (i0 + r) * kSidePitch + j0) = make_float4(s[r][0], s[r][1], s[r][2], s[r][3]);
-    };
-    for (int t = 0; t < steps; ++t) {
-        float s[4][4] = {}, m[4][4] = {};
-        if (in) small_product(s, A, A, k_end, i0, j0);
+    __device__ __forceinline__ void put(float* shares, int i0, int j0) const {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                m[r][e] = __fmaf_rn(c, s[r][e], __fmaf_rn(b, A[(i0 + r) * kSidePitch + j0 + e], i0 + r == j0 + e ? a : 0.0f));
-        keep(M, m);
-        __syncthreads();
-        float u[4][4] = {}, v[4][4] = {};
-        if (in) small_product(u, M, P, k_end, i0, j0);
-        if (in) small_product(v, M, M, k_end, i0, j0);
-        keep(S, v);
-        __syncthreads();
-        keep(P, u);
-        float w[4][4] = {};
-        if (in) small_product(w, S, A, k_end, i0, j0);
-        __syncthreads();
-        keep(A, w);
-        __syncthreads();
+            *reinterpret_cast<float4*>(shares + ((int64_t)blockIdx.x * kSide + i0 + r) * kSide + j0) = make_float4(s[r][0], s[r][1], s[r][2], s[r][3]);
     }
-    for (int e = threadIdx.x; e < kSide * kSide; e += kNarrowThreads)
-        poly[e] = e / kSide < p && e % kSide < p ? P[e / kSide * kSidePitch + e % kSide] * scale : 0.0f;
-}
+};
 
-// out = P X_0, kChunk columns (rows, where tall) at a time.
+// X_0 in blocks of columns, [block][p][kChunk], and the shares of its A.
 template <typename T>
-__global__ void __launch_bounds__(kNarrowThreads) narrow_apply_kernel(Mat x, int tall, int p, int64_t q, const float* parts, double eps,
-                                                                      const float* poly, Mat out) {
-    __shared__ __align__(16) float chunk[kChunk * kSidePitch], box[kSideValues];
+__global__ void __launch_bounds__(kNarrowThreads) narrow_first_kernel(Mat x, int tall, int p, int64_t q, const float* parts, double eps, float* held,
+                                                                      float* shares) {
+    __shared__ __align__(16) float columns[kChunk * kSidePitch];
     wait_for_previous();
     const float2 f = norm_factor(parts, eps, 1.0f);
-    for (int e = threadIdx.x; e < kSide * kSide; e += kNarrowThreads) box[e % kSide * kSidePitch + e / kSide] = poly[e];
+    const T* data = static_cast<const T*>(x.data);
     const int i0 = threadIdx.x / 16 * 4, j0 = threadIdx.x % 16 * 4;
-    for (int64_t j = (int64_t)blockIdx.x * kChunk; j < q; j += (int64_t)gridDim.x * kChunk) {
-        // [k][j]: the chunk transposed
-        const T* data = static_cast<const T*>(x.data);
-        __syncthreads();
+    GramShare share;
+    for (int64_t block = blockIdx.x; block * kChunk < q; block += gridDim.x) {
+        const int64_t first = block * kChunk;
         for (int c = threadIdx.x; c < kSide * kChunk; c += kNarrowThreads) {
-            const int i = tall ? c % kSide : c / kChunk, jj = tall ? c / kSide : c % kChunk;
+            const int i = tall ? c % kSide : c / kChunk, j = tall ? c / kSide : c % kChunk;
             float v = 0.0f;
-            if (i < p && j + jj < q) v = value_of(tall ? data + (j + jj) * x.stride + i : data + i * x.stride + j + jj) * f.x * f.y;
-            chunk[i * kSidePitch + jj] = v;
+            if (i < p && first + j < q) v = value_of(tall ? data + (first + j) * x.stride + i : data + i * x.stride + first + j) * f.x * f.y;
+            columns[j * kSidePitch + i] = v;
         }
         __syncthreads();
-        if (i0 >= p) continue;
+        for (int c = threadIdx.x; c < p * kChunk; c += kNarrowThreads) held[block * p * kChunk + c] = columns[c % kChunk * kSidePitch + c / kChunk];
+        share.add(columns, p, i0, j0);
+        __syncthreads();
+    }
+    share.put(shares, i0, j0);
+}
+
+// A from its shares: 16 values a block of threads, 16 threads a value.
+constexpr int kSumValues = 16, kSumBlocks = kSide * kSide / kSumValues;
+__global__ void __launch_bounds__(kNarrowThreads) narrow_sum_kernel(const float* shares, int n_shares, float* gram) {
+    __shared__ float box[kNarrowThreads];
+    wait_for_previous();
+    const int e = blockIdx.x * kSumValues + threadIdx.x % kSumValues;
+    float sum = 0.0f;
+#pragma unroll 8
+    for (int k = threadIdx.x / kSumValues; k < n_shares; k += kNarrowThreads / kSumValues) sum += shares[(int64_t)k * kSide * kSide + e];
+    box[threadIdx.x] = sum;
+    __syncthreads();
+    if (threadIdx.x < kSumValues) {
+        float total = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kNarrowThreads; k += kSumValues) total += box[threadIdx.x + k];
+        gram[e] = total;
+    }
+}
+
+// X <- a X + (b A + c A A) X and the shares of the next A; in the last step
+// scale * X to the caller's matrix.
+__global__ void __launch_bounds__(kNarrowThreads) narrow_step_kernel(float* held, int tall, int p, int64_t q, const float* gram, float a, float b, float c,
+                                                                     float scale, float* shares, Mat out) {
+    extern __shared__ __align__(16) float room[];
+    float *M = room, *now = room + kSideValues, *next = room + 2 * kSideValues;
+    wait_for_previous();
+    const int i0 = threadIdx.x / 16 * 4, j0 = threadIdx.x % 16 * 4, k_end = (p + 3) / 4 * 4;
+    for (int e = threadIdx.x; e < kSide * kSide; e += kNarrowThreads) now[e / kSide * kSidePitch + e % kSide] = gram[e];
+    __syncthreads();
+    float m[4][4] = {};
+    if (i0 < p && j0 < p) small_product(m, now, now, k_end, i0, j0);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            M[(i0 + r) * kSidePitch + j0 + e] = __fmaf_rn(c, m[r][e], __fmaf_rn(b, now[(i0 + r) * kSidePitch + j0 + e], i0 + r == j0 + e ? a : 0.0f));
+    GramShare share;
+    for (int64_t block = blockIdx.x; block * kChunk < q; block += gridDim.x) {
+        const int64_t first = block * kChunk;
+        float* at_block = held + block * p * kChunk;
+        __syncthreads();
+        for (int e = threadIdx.x; e < kSide * kChunk / 4; e += kNarrowThreads) {
+            const int i = e / (kChunk / 4), j = e % (kChunk / 4) * 4;
+            *reinterpret_cast<float4*>(now + i * kSidePitch + j) =
+                i < p ? *reinterpret_cast<const float4*>(at_block + i * kChunk + j) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+        __syncthreads();
         float s[4][4] = {};
-        small_product(s, box, chunk, p, i0, j0);
+        if (i0 < p) small_product(s, M, now, k_end, i0, j0);
+        if (!out.data) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (i0 + r < p) *reinterpret_cast<float4*>(at_block + (i0 + r) * kChunk + j0) = make_float4(s[r][0], s[r][1], s[r][2], s[r][3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                *reinterpret_cast<float4*>(next + (j0 + e) * kSidePitch + i0) = make_float4(s[0][e], s[1][e], s[2][e], s[3][e]);
+            __syncthreads();
+            share.add(next, p, i0, j0);
+            continue;
+        }
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int e = 0; e < 4; ++e) {
                 const int i = i0 + r;
-                const int64_t jj = j + j0 + c;
-                if (i < p && jj < q) {
-                    uint16_t* to = tall ? at(out, jj, i) : at(out, i, jj);
-                    *to = (uint16_t)f32_to_bf16(s[r][c]);
-                }
+                const int64_t j = first + j0 + e;
+                if (i < p && j < q) *(tall ? at(out, j, i) : at(out, i, j)) = (uint16_t)f32_to_bf16(s[r][e] * scale);
             }
     }
+    if (!out.data) share.put(shares, i0, j0);
 }
 
 // -------------------------------------------------------------- epilogues
@@ -340,29 +347,34 @@ struct Next {
 
 constexpr size_t kPartsRoom = (3 * kSquareBlocks * 4 + 255) / 256 * 256;
 
-constexpr size_t kNarrowRoom = (size_t)(kGramBlocks + 1) * kSide * kSide * 4;
+// Blocks of columns, shares of A, and their room with A and X.
+int64_t narrow_blocks(int64_t q) { return (q + kChunk - 1) / kChunk; }
+int64_t narrow_shares(int64_t q) { return std::min<int64_t>(narrow_blocks(q), kGramBlocks); }
+size_t narrow_room(int64_t p, int64_t q) { return (size_t)((narrow_shares(q) + 1) * kSide * kSide + narrow_blocks(q) * kChunk * p) * 4; }
 
 template <typename T>
 cudaError_t narrow(const OrthoArgs& a, cudaStream_t s) {
-    const bool tall = a.rows > a.cols;
+    const int tall = a.rows > a.cols;
     const int p = (int)(tall ? a.cols : a.rows);
-    const int64_t q = tall ? a.rows : a.cols, chunks = (q + kChunk - 1) / kChunk;
+    const int64_t q = tall ? a.rows : a.cols;
+    const int n_shares = (int)narrow_shares(q);
     const float* parts = reinterpret_cast<const float*>(a.work);
-    float* grams = reinterpret_cast<float*>(a.work + kPartsRoom);
-    float* poly = grams + (size_t)kGramBlocks * kSide * kSide;
-    const int n_parts = (int)std::min<int64_t>(chunks, kGramBlocks);
+    float* shares = reinterpret_cast<float*>(a.work + kPartsRoom);
+    float* gram = shares + (size_t)n_shares * kSide * kSide;
+    float* held = gram + kSide * kSide;
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = allow_smem(reinterpret_cast<const void*>(narrow_steps_kernel), 4 * kSideValues * 4, done);
-    if (e == cudaSuccess) e = launch_next(narrow_gram_kernel<T>, dim3(n_parts), kNarrowThreads, 0, s, a.x, (int)tall, p, q, parts, a.eps, grams);
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(narrow_step_kernel), kNarrowSmem, done);
+    if (e == cudaSuccess) e = launch_next(narrow_first_kernel<T>, dim3(n_shares), kNarrowThreads, 0, s, a.x, tall, p, q, parts, a.eps, held, shares);
     count_launch();
-    if (e == cudaSuccess)
-        e = launch_next(narrow_steps_kernel, dim3(1), kNarrowThreads, 4 * kSideValues * 4, s, (const float*)grams, n_parts, p, a.steps, a.a, a.b, a.c,
-                        a.scale, poly);
-    count_launch();
-    const int grid = (int)std::min<int64_t>(chunks, 4 * sm_count());
-    if (e == cudaSuccess)
-        e = launch_next(narrow_apply_kernel<T>, dim3(grid), kNarrowThreads, 0, s, a.x, (int)tall, p, q, parts, a.eps, (const float*)poly, a.out);
-    count_launch();
+    for (int t = 0; t < a.steps && e == cudaSuccess; ++t) {
+        const Mat out = t + 1 == a.steps ? a.out : Mat{nullptr, 0};
+        e = launch_next(narrow_sum_kernel, dim3(kSumBlocks), kNarrowThreads, 0, s, (const float*)shares, n_shares, gram);
+        count_launch();
+        if (e == cudaSuccess)
+            e = launch_next(narrow_step_kernel, dim3(n_shares), kNarrowThreads, kNarrowSmem, s, held, tall, p, q, (const float*)gram, a.a, a.b, a.c, a.scale,
+                            shares, out);
+        count_launch();
+    }
     return e;
 }
 
@@ -389,7 +401,7 @@ size_t sums_bytes(int64_t rows, int64_t cols) {
 size_t ortho_bytes(int64_t rows, int64_t cols) {
     if (rows == 0 || cols == 0) return 0;
     const int64_t p = rows < cols ? rows : cols;
-    if (p <= kSide) return kPartsRoom + kNarrowRoom;
+    if (p <= kSide) return kPartsRoom + narrow_room(p, std::max(rows, cols));
     return kPartsRoom + 3 * aligned_room(rows, cols) + 2 * aligned_room(p, p) + sums_bytes(rows, cols);
 }
 

@@ -1,0 +1,62 @@
+"""fsdp_orthogonalize over steps, polynomials and kinds of matrices against its
+definition in 64 bits (products_ref).
+
+Tolerances, in the 2-norm relative to the result. Rounding the result to
+bfloat16: 2^-8 over the square root of 3, 2.3e-3. With at most 64 rows or
+columns X is held in binary32: a step leaves in each element an error of the
+order of 2^-24 of the terms that it sums, (|a| + |b| + |c|) |X| / sqrt(p q) for
+singular values near one at most, and errors of elements that are independent
+have singular values of at most (sqrt(p) + sqrt(q)) of theirs. A direction in
+which x has a singular value s sees that relative to s / |x|; the steps lift
+both alike, and those after the first, whose X has grown, add less than half of
+what the steps before them added. Four times that is allowed for."""
+import pytest
+import torch
+
+import products_ref as R
+from test_gpu_products import BF16, F32, matrix, no_wait_ran_out, ortho  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+DEFAULT, CUBIC, QUINTIC = (3.4445, -4.7750, 2.0315), (1.5, -0.5, 0.0), (1.875, -1.25, 0.375)
+ROUNDED = 2.3e-3
+
+
+def held_in_32_bits(x, coefficients):
+    s = torch.linalg.svdvals(R.d(x))
+    p, q = min(x.shape), max(x.shape)
+    spread = float(s.square().sum().sqrt() / s.min())
+    return ROUNDED + 4 * sum(map(abs, coefficients)) * 2.0 ** -24 * (p ** 0.5 + q ** 0.5) / (p * q) ** 0.5 * spread
+
+
+@pytest.mark.parametrize("steps, coefficients", [(7, DEFAULT), (8, DEFAULT), (9, DEFAULT), (12, DEFAULT), (16, QUINTIC), (24, QUINTIC), (40, QUINTIC),
+                                                 (25, CUBIC), (30, CUBIC), (64, CUBIC)])
+@pytest.mark.parametrize("rows, cols", [(64, 200), (200, 64), (33, 70), (12, 3000)])
+def test_few_rows_over_many_steps(rows, cols, steps, coefficients):
+    for kind in ("noise", "low"):
+        x = matrix(kind, rows, cols, F32)
+        got = ortho(x, steps=steps, coefficients=coefficients)
+        assert R.distance(got, R.orthogonalize(x, steps, coefficients)) < held_in_32_bits(x, coefficients)
+
+
+@pytest.mark.parametrize("steps, coefficients, most", [(5, DEFAULT, 1.21), (10, DEFAULT, 1.21), (30, DEFAULT, 1.21), (64, DEFAULT, 1.21), (24, QUINTIC, 1.0),
+                                                       (64, QUINTIC, 1.0), (40, CUBIC, 1.0)])
+@pytest.mark.parametrize("rows, cols", [(8, 512), (64, 1024), (1024, 64)])
+def test_matrices_without_full_rank_stay_bounded(rows, cols, steps, coefficients, most):
+    # rows that repeat: the rank is 2, exactly. In the other directions there is what rounding
+    # leaves, which the steps lift as they lift anything else: the polynomials map [0, most] into itself.
+    few, many = min(rows, cols), max(rows, cols)
+    base, which = matrix("noise", 2, many, F32), torch.arange(few, device="cuda") % 2
+    x = base[which].contiguous()
+    got = R.d(ortho(x if rows <= cols else x.t().contiguous(), steps=steps, coefficients=coefficients))
+    got = got if rows <= cols else got.T
+    # rounding to bfloat16 moves singular values by its norm, ROUNDED of |out|, at most
+    slack = ROUNDED * float(got.norm()) + 1e-3
+    assert bool(torch.isfinite(got).all())
+    assert float(torch.linalg.eigvalsh(got @ got.T).max().sqrt()) < most + slack
+    if coefficients != DEFAULT:
+        # x = U (D base) with U's columns orthonormal, and these polynomials bring D base to its nearest orthonormal rows
+        U = (which.cpu()[:, None] == torch.arange(2)) / (few / 2) ** 0.5
+        s, v = torch.linalg.eigh(R.d(base) @ R.d(base).T)
+        nearest = v @ torch.diag(s ** -0.5) @ v.T @ R.d(base)
+        assert float((U.double().T @ got - nearest).norm()) < slack
