@@ -56,59 +56,68 @@ __device__ __forceinline__ void put_planes(const Mat& hi, const Mat& lo, int64_t
 // ------------------------------------------------------- the first iterate
 
 // A block's sums of squares, of values by their size, so that no square
-// overflows or vanishes: those of at least 2^60 by 2^-64, those below 2^-50 by
-// 2^64 (Blue, "A portable Fortran program to find the Euclidean norm of a
-// vector", 1978).
+// overflows or vanishes: those of at least 2^50 by 2^-90, those below 2^-40 by
+// 2^90 (Blue, "A portable Fortran program to find the Euclidean norm of a
+// vector", 1978). The squares lie between 2^-118 and 2^100, so binary32 holds a
+// thread's next 64 granules' sums of any of the three; beyond that they are
+// added up in 64 bits, which no number of values overflows or wears out.
 template <typename T>
-__global__ void __launch_bounds__(kSquareThreads) square_kernel(Mat x, int64_t rows, int64_t cols, float* parts) {
+__global__ void __launch_bounds__(kSquareThreads) square_kernel(Mat x, int64_t rows, int64_t cols, double* parts) {
     wait_for_previous();
     const int64_t per = (cols + kGran - 1) / kGran, all_granules = rows * per;
-    float sum[3] = {0.0f, 0.0f, 0.0f};
-    for (int64_t g = (int64_t)blockIdx.x * kSquareThreads + threadIdx.x; g < all_granules; g += (int64_t)kSquareBlocks * kSquareThreads) {
-        const int64_t row = g / per, i = g - row * per;
-        Raw<T> r;
-        load_granule(r, static_cast<const T*>(x.data) + row * x.stride, i * kGran, granule_cols(i, cols));
-        const Cols v = widened(r);
+    double total[3] = {0.0, 0.0, 0.0};
+    int64_t g = (int64_t)blockIdx.x * kSquareThreads + threadIdx.x;
+    while (g < all_granules) {
+        float sum[3] = {0.0f, 0.0f, 0.0f};
+        for (int n = 0; n < 64 && g < all_granules; ++n, g += (int64_t)kSquareBlocks * kSquareThreads) {
+            const int64_t row = g / per, i = g - row * per;
+            Raw<T> r;
+            load_granule(r, static_cast<const T*>(x.data) + row * x.stride, i * kGran, granule_cols(i, cols));
+            const Cols v = widened(r);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float f = v.get(e), m = fabsf(f);
-            const int which = m >= 0x1p60f ? 2 : (m < 0x1p-50f ? 0 : 1);
-            const float q = which == 2 ? f * 0x1p-64f : (which == 0 ? f * 0x1p64f : f);
-            sum[0] = which == 0 ? __fmaf_rn(q, q, sum[0]) : sum[0];
-            sum[2] = which == 2 ? __fmaf_rn(q, q, sum[2]) : sum[2];
-            sum[1] = which == 1 ? __fmaf_rn(q, q, sum[1]) : sum[1];  // NaN too
+            for (int e = 0; e < 8; ++e) {
+                const float f = v.get(e), m = fabsf(f);
+                const int which = m >= 0x1p50f ? 2 : (m < 0x1p-40f ? 0 : 1);
+                const float q = which == 2 ? f * 0x1p-90f : (which == 0 ? f * 0x1p90f : f);
+                sum[0] = which == 0 ? __fmaf_rn(q, q, sum[0]) : sum[0];
+                sum[2] = which == 2 ? __fmaf_rn(q, q, sum[2]) : sum[2];
+                sum[1] = which == 1 ? __fmaf_rn(q, q, sum[1]) : sum[1];  // NaN too
+            }
         }
+#pragma unroll
+        for (int k = 0; k < 3; ++k) total[k] += (double)sum[k];
     }
-    __shared__ float box[3][kSquareThreads / 32];
+    __shared__ double box[3][kSquareThreads / 32];
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-        sum[k] = warp_sum(sum[k]);
-        if (threadIdx.x % 32 == 0) box[k][threadIdx.x / 32] = sum[k];
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) total[k] += __shfl_xor_sync(kFull, total[k], d);
+        if (threadIdx.x % 32 == 0) box[k][threadIdx.x / 32] = total[k];
     }
     __syncthreads();
     if (threadIdx.x < 3) {
-        float total = 0.0f;
-        for (int w = 0; w < kSquareThreads / 32; ++w) total += box[threadIdx.x][w];
-        parts[threadIdx.x * kSquareBlocks + blockIdx.x] = total;
+        double of_block = 0.0;
+        for (int w = 0; w < kSquareThreads / 32; ++w) of_block += box[threadIdx.x][w];
+        parts[threadIdx.x * kSquareBlocks + blockIdx.x] = of_block;
     }
 }
 
 // lift / (|x| + eps) from the parts, as a product of two factors neither of
 // which leaves binary32's range. All threads of a block of at least 96 take
 // part.
-__device__ __forceinline__ float2 norm_factor(const float* parts, double eps, float lift) {
+__device__ __forceinline__ float2 norm_factor(const double* parts, double eps, float lift) {
     __shared__ double sums[3];
     __shared__ float2 factor;
     if (threadIdx.x < 96) {
         double s = 0.0;
-        for (int i = threadIdx.x % 32; i < kSquareBlocks; i += 32) s += (double)parts[threadIdx.x / 32 * kSquareBlocks + i];
+        for (int i = threadIdx.x % 32; i < kSquareBlocks; i += 32) s += parts[threadIdx.x / 32 * kSquareBlocks + i];
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
         if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = s;
     }
     __syncthreads();
     if (threadIdx.x == 0) {
-        const double norm = sqrt(sums[0] * 0x1p-128 + sums[1] + sums[2] * 0x1p128);
+        const double norm = sqrt(sums[0] * 0x1p-180 + sums[1] + sums[2] * 0x1p180);
         const double f = (double)lift / (norm + eps);
         int e = 0;
         const double m = frexp(f, &e);
@@ -120,7 +129,7 @@ __device__ __forceinline__ float2 norm_factor(const float* parts, double eps, fl
 
 // X = x / (|x| + eps) as two planes scaled by `lift`.
 template <typename T>
-__global__ void __launch_bounds__(256) planes_kernel(Mat x, int64_t rows, int64_t cols, const float* parts, double eps, float lift, Mat hi,
+__global__ void __launch_bounds__(256) planes_kernel(Mat x, int64_t rows, int64_t cols, const double* parts, double eps, float lift, Mat hi,
                                                      Mat lo) {
     wait_for_previous();
     const float2 f = norm_factor(parts, eps, lift);
@@ -186,7 +195,7 @@ struct GramShare {
 
 // X_0 in blocks of columns, [block][p][kChunk], and the shares of its A.
 template <typename T>
-__global__ void __launch_bounds__(kNarrowThreads) narrow_first_kernel(Mat x, int tall, int p, int64_t q, const float* parts, double eps, float* held,
+__global__ void __launch_bounds__(kNarrowThreads) narrow_first_kernel(Mat x, int tall, int p, int64_t q, const double* parts, double eps, float* held,
                                                                       float* shares) {
     __shared__ __align__(16) float columns[kChunk * kSidePitch];
     wait_for_previous();
@@ -345,7 +354,7 @@ struct Next {
     }
 };
 
-constexpr size_t kPartsRoom = (3 * kSquareBlocks * 4 + 255) / 256 * 256;
+constexpr size_t kPartsRoom = (3 * kSquareBlocks * 8 + 255) / 256 * 256;
 
 // Blocks of columns, shares of A, and their room with A and X.
 int64_t narrow_blocks(int64_t q) { return (q + kChunk - 1) / kChunk; }
@@ -358,7 +367,7 @@ cudaError_t narrow(const OrthoArgs& a, cudaStream_t s) {
     const int p = (int)(tall ? a.cols : a.rows);
     const int64_t q = tall ? a.rows : a.cols;
     const int n_shares = (int)narrow_shares(q);
-    const float* parts = reinterpret_cast<const float*>(a.work);
+    const double* parts = reinterpret_cast<const double*>(a.work);
     float* shares = reinterpret_cast<float*>(a.work + kPartsRoom);
     float* gram = shares + (size_t)n_shares * kSide * kSide;
     float* held = gram + kSide * kSide;
@@ -411,7 +420,7 @@ cudaError_t launch_ortho(int dt, const OrthoArgs& a, cudaStream_t s) {
     const int64_t p = tall ? a.cols : a.rows, q = tall ? a.rows : a.cols;
     const size_t plane = aligned_room(a.rows, a.cols);
     const int64_t ld = whole_granules(a.cols), lp = whole_granules(p);
-    float* parts = reinterpret_cast<float*>(a.work);
+    double* parts = reinterpret_cast<double*>(a.work);
     char* w = a.work + kPartsRoom;
     Mat hi = {w, ld}, next = {w + plane, ld};
     const Mat lo = {w + 2 * plane, ld}, gram = {w + 3 * plane, lp}, poly = {w + 3 * plane + aligned_room(p, p), lp};
@@ -435,8 +444,8 @@ cudaError_t launch_ortho(int dt, const OrthoArgs& a, cudaStream_t s) {
     if (p <= kSide) return dt == FSDP_F32 ? narrow<float>(a, s) : narrow<uint16_t>(a, s);
     const int64_t granules = a.rows * ((a.cols + kGran - 1) / kGran);
     const int grid = (int)std::min<int64_t>((granules + 255) / 256, 8 * sm_count());
-    e = dt == FSDP_F32 ? launch_next(planes_kernel<float>, dim3(grid), 256, 0, s, a.x, a.rows, a.cols, (const float*)parts, a.eps, lift, hi, lo)
-                       : launch_next(planes_kernel<uint16_t>, dim3(grid), 256, 0, s, a.x, a.rows, a.cols, (const float*)parts, a.eps, lift, hi, lo);
+    e = dt == FSDP_F32 ? launch_next(planes_kernel<float>, dim3(grid), 256, 0, s, a.x, a.rows, a.cols, (const double*)parts, a.eps, lift, hi, lo)
+                       : launch_next(planes_kernel<uint16_t>, dim3(grid), 256, 0, s, a.x, a.rows, a.cols, (const double*)parts, a.eps, lift, hi, lo);
     count_launch();
     for (int i = 0; i < a.steps && e == cudaSuccess; ++i) {
         const float shift = i + 2 < a.steps ? a.a : 0.5f * (1.0f + a.a);

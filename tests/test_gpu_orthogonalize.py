@@ -2,7 +2,9 @@
 definition in 64 bits (products_ref).
 
 Tolerances, in the 2-norm relative to the result. Rounding the result to
-bfloat16: 2^-8 over the square root of 3, 2.3e-3. With at most 64 rows or
+bfloat16: 2^-8 over the square root of 3, 2.3e-3. With more than 64 rows and
+columns each step rounds four factors to binary16, which reaches the result as
+2^-11 a step (test_gpu_products). With at most 64 rows or
 columns X is held in binary32: a step leaves in each element an error of the
 order of 2^-24 of the terms that it sums, (|a| + |b| + |c|) |X| / sqrt(p q) for
 singular values near one at most, and errors of elements that are independent
@@ -10,6 +12,8 @@ have singular values of at most (sqrt(p) + sqrt(q)) of theirs. A direction in
 which x has a singular value s sees that relative to s / |x|; the steps lift
 both alike, and those after the first, whose X has grown, add less than half of
 what the steps before them added. Four times that is allowed for."""
+import math
+
 import pytest
 import torch
 
@@ -20,6 +24,7 @@ pytestmark = pytest.mark.gpu
 
 DEFAULT, CUBIC, QUINTIC = (3.4445, -4.7750, 2.0315), (1.5, -0.5, 0.0), (1.875, -1.25, 0.375)
 ROUNDED = 2.3e-3
+HELD_IN_16_BITS = ROUNDED + 5 * 2.0 ** -11  # five steps
 
 
 def held_in_32_bits(x, coefficients):
@@ -60,3 +65,33 @@ def test_matrices_without_full_rank_stay_bounded(rows, cols, steps, coefficients
         s, v = torch.linalg.eigh(R.d(base) @ R.d(base).T)
         nearest = v @ torch.diag(s ** -0.5) @ v.T @ R.d(base)
         assert float((U.double().T @ got - nearest).norm()) < slack
+
+
+@pytest.mark.parametrize("rows, cols", [(64, 3000), (1000, 1000)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("std", [1e-43, 1e-40, 1e-37, 1e-25, 1e-13, 1e-12, 1e15, 2e15, 5e17, 3e18, 1e36, 5e37])
+def test_any_finite_values(rows, cols, dtype, std):
+    # the sums of squares of these reach from 2^-290 to 2^270. A value of 1e-43 is up to 71 steps of the
+    # smallest one of float32, and none of bfloat16.
+    if dtype == BF16 and std < 1e-40:
+        return
+    x = matrix("noise", rows, cols, dtype, std=std)
+    assert bool(torch.isfinite(x).all()) and bool(x.any())
+    assert R.distance(ortho(x, eps=0.0), R.orthogonalize(x, eps=0.0)) < HELD_IN_16_BITS
+
+
+@pytest.mark.parametrize("rows, cols", [(40, 70), (100, 130), (130, 100)])
+def test_one_large_value_among_small_ones(rows, cols):
+    x = matrix("noise", rows, cols, F32, std=1e-20)
+    x[3, 5] = 3e38
+    got = ortho(x, eps=0.0)
+    assert R.distance(got, R.orthogonalize(x, eps=0.0)) < HELD_IN_16_BITS
+
+
+@pytest.mark.parametrize("rows, cols", [(100, 130), (130, 100), (300, 300)])
+def test_infinities_and_nan(rows, cols):
+    for bad in (math.inf, -math.inf, math.nan):
+        x = matrix("noise", rows, cols, F32).clone()
+        x[7, 9] = bad
+        assert bool(torch.isnan(ortho(x)).all())
+    assert not bool(ortho(torch.zeros(rows, cols, device="cuda")).any())
