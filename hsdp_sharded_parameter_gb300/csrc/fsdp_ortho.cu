@@ -118,7 +118,9 @@ __device__ __forceinline__ float2 norm_factor(const double* parts, double eps, f
     __syncthreads();
     if (threadIdx.x == 0) {
         const double norm = sqrt(sums[0] * 0x1p-180 + sums[1] + sums[2] * 0x1p180);
-        const double f = (double)lift / (norm + eps);
+        // a norm is 0 or at least 2^-149: a quotient above 2^165 has only zeros to scale (without an eps it is 0 / 0)
+        double f = (double)lift / (norm + eps);
+        if (norm + eps > 0.0) f = fmin(f, 0x1p200);
         int e = 0;
         const double m = frexp(f, &e);
         factor = isfinite(f) ? make_float2(ldexpf(1.0f, e / 2), (float)ldexp(m, e - e / 2)) : make_float2((float)f, 1.0f);

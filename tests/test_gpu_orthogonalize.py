@@ -95,3 +95,9 @@ def test_infinities_and_nan(rows, cols):
         x[7, 9] = bad
         assert bool(torch.isnan(ortho(x)).all())
     assert not bool(ortho(torch.zeros(rows, cols, device="cuda")).any())
+
+
+@pytest.mark.parametrize("rows, cols", [(40, 70), (100, 130)])
+@pytest.mark.parametrize("eps", [5e-324, 1e-300, 1e-40, 1.0, 1e300])
+def test_zeros_stay_zeros(rows, cols, eps):
+    assert not bool(ortho(torch.zeros(rows, cols, device="cuda"), eps=eps).any())
