@@ -702,8 +702,10 @@ def fsdp_orthogonalize_workspace(rows, cols):
 def fsdp_orthogonalize(x, out, workspace, steps=5, coefficients=(3.4445, -4.7750, 2.0315), scale=1.0, eps=1e-7, stream=None):
     """out = scale * X after `steps` Newton-Schulz steps from X = x / (|x| + eps):
     with A = X X^T, X <- a X + (b A + c A A) X. x: a matrix of float32 or
-    bfloat16; out: the same shape in bfloat16. workspace: a tensor of at least
-    fsdp_orthogonalize_workspace(rows, cols) bytes."""
+    bfloat16; out: the same shape in bfloat16. The coefficients have to keep
+    singular values that start in [0, 1] at or below 8 until the last step.
+    workspace: a tensor of at least fsdp_orthogonalize_workspace(rows, cols)
+    bytes."""
     what = "orthogonalize"
     xp, rows, cols, xs, dt, dev = _matrix(what, "x", x)
     op, os_ = _like(what, "out", out, rows, cols, FSDP_BF16, dev)

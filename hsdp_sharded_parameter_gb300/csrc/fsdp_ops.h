@@ -121,6 +121,10 @@ size_t ffn_most_bytes(int64_t tokens, int64_t hidden, int64_t inner, bool aligne
 size_t ffn_grad_bytes(const FfnGradArgs& a);
 size_t ffn_grad_most_bytes(int64_t tokens, int64_t hidden, int64_t inner, bool aligned);
 size_t ortho_bytes(int64_t rows, int64_t cols);
+// The largest singular value that any of the steps may start from, those of the
+// first iterate being at most 1; the scales allow for kMostReach.
+double ortho_reach(int steps, double a, double b, double c);
+constexpr double kMostReach = 8.0;
 
 // Each enqueues its kernels (counting them) and returns the launches' error.
 cudaError_t launch_embedding(int table_dt, int out_dt, const EmbeddingArgs& a, cudaStream_t s);

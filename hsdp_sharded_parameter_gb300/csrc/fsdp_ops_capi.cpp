@@ -395,6 +395,8 @@ int fsdp_orthogonalize(int64_t rows, int64_t cols, int dt, const void* x, int64_
     if (steps < 1 || steps > 64) return bad(what, "steps is not in [1, 64]");
     for (const double v : {a, b, c})
         if (!(std::fabs(v) <= 256.0)) return bad(what, "a coefficient is not in [-256, 256]");
+    if (!(ortho_reach(steps, a, b, c) <= kMostReach * (1 + 1e-6)))
+        return bad(what, "the coefficients take a singular value above 8 before the last step");
     FSDP_TRY(check_float(what, "scale", scale));
     if (!(eps >= 0.0 && std::isfinite(eps))) return bad(what, "eps is negative or not finite");
     FSDP_TRY(check_work(what, workspace, workspace_bytes, ortho_bytes(rows, cols)));

@@ -390,6 +390,7 @@ cudaError_t narrow(const OrthoArgs& a, cudaStream_t s) {
 }
 
 int log2_near(double v) { return (int)std::nearbyint(std::log2(v)); }
+int log2_above(double v) { return (int)std::ceil(std::log2(v)); }
 
 // The products of a step; which factor's rows are neighbours in memory goes by
 // the longer side.
@@ -416,6 +417,23 @@ size_t ortho_bytes(int64_t rows, int64_t cols) {
     return kPartsRoom + 3 * aligned_room(rows, cols) + 2 * aligned_room(p, p) + sums_bytes(rows, cols);
 }
 
+double ortho_reach(int steps, double a, double b, double c) {
+    double reach = 1.0;
+    for (int t = 1; t < steps && reach <= kMostReach * 2; ++t) {
+        // the most of |a s + b s^3 + c s^5| for s in [0, reach]: at its end or where the derivative, a polynomial of s^2, is 0
+        const double u = reach * reach, root = 9.0 * b * b - 20.0 * a * c;
+        double at[3] = {u, 0.0, 0.0};
+        if (root >= 0.0) {
+            const double half = -0.5 * (3.0 * b + std::copysign(std::sqrt(root), b));
+            if (c != 0.0) at[1] = half / (5.0 * c);
+            if (half != 0.0) at[2] = a / half;
+        }
+        for (const double v : at)
+            if (v > 0.0 && v <= u) reach = std::max(reach, std::fabs(std::sqrt(v) * (a + b * v + c * v * v)));
+    }
+    return reach;
+}
+
 cudaError_t launch_ortho(int dt, const OrthoArgs& a, cudaStream_t s) {
     if (a.rows == 0 || a.cols == 0) return cudaSuccess;
     const bool tall = a.rows > a.cols;
@@ -429,12 +447,14 @@ cudaError_t launch_ortho(int dt, const OrthoArgs& a, cudaStream_t s) {
     float* sums = reinterpret_cast<float*>(w + 3 * plane + 2 * aligned_room(p, p));
     // Scales by powers of two that keep values in binary16's normal range: X's
     // elements are about 1/sqrt(p q) at first and 1/sqrt(q) at the end, never
-    // above about 1.2; A's diagonal about 1/p at first; the polynomial's at most
-    // |a| + 1.5 |b| + 2.25 |c|.
-    const int sx = log2_near(std::sqrt((double)q));
-    const int sa = std::min(13, log2_near((double)p));
-    const double most = std::fabs(a.a) + 1.5 * std::fabs(a.b) + 2.25 * std::fabs(a.c);
-    const int sb = std::min(sa, 15 - (int)std::ceil(std::log2(std::max(most, 1.0))));
+    // above the largest singular value, `reach`; A's diagonal is about 1/p at
+    // first, and nothing in it above reach^2; the polynomial's at most |a| +
+    // |b| reach^2 + |c| reach^4.
+    const double reach = std::max(ortho_reach(a.steps, a.a, a.b, a.c), std::sqrt(1.5)), square = reach * reach;
+    const int sx = std::min(log2_near(std::sqrt((double)q)), 15 - log2_above(reach));
+    const int sa = std::min({13, log2_near((double)p), 15 - log2_above(square)});
+    const double most = std::fabs(a.a) + square * std::fabs(a.b) + square * square * std::fabs(a.c);
+    const int sb = std::min(sa, 15 - log2_above(std::max(most, 1.0)));
     const float lift = std::ldexp(1.0f, sx);
     if (dt == FSDP_F32)
         square_kernel<float><<<kSquareBlocks, kSquareThreads, 0, s>>>(a.x, a.rows, a.cols, parts);

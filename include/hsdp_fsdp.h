@@ -575,11 +575,19 @@ int fsdp_orthogonalize_workspace(int64_t rows, int64_t cols, size_t* bytes);
  *   X <- a X + (b A + c A A) X,
  * and out = scale * X. With the coefficients (3.4445, -4.7750, 2.0315) five
  * steps bring x's larger singular values to between about 0.7 and 1.2. x has
- * type dt, out is bfloat16. Inside, X is held in 22 bits and A and the
- * polynomial in binary16 under a power of two: out is off by about half a step
- * of bfloat16 more than its own rounding. A sum of the squares of x that
- * binary32 does not hold is no limit; x with infinities or NaN gives NaN; x = 0
- * gives 0 for eps > 0. 1 <= steps <= 64; |a|, |b|, |c| <= 256; eps >= 0. */
+ * type dt, out is bfloat16. Where x has more than 64 rows and columns, X is held
+ * in 22 bits and A and the polynomial in binary16 under a power of two, and up
+ * to a dozen steps put out off by up to 2^-11 each, in the 2-norm, beside its own
+ * rounding (five steps 0.0020 in all on noise, twelve 0.0046); else everything
+ * is in binary32. Directions in which x has next to nothing hold what rounding
+ * left there, as they do in any arithmetic, and the steps lift that as they lift
+ * anything, by up to |a| each: with these coefficients 2^-22 of |x| is 2^-13
+ * after five steps and all of a direction after thirteen.
+ * The norm is that of any finite x; x with infinities or NaN gives NaN; x = 0
+ * gives 0 for eps > 0. 1 <= steps <= 64; |a|, |b|, |c| <= 256, and no singular
+ * value in [0, 1] may come to more than 8 before the last step, by the
+ * polynomial a s + b s^3 + c s^5 applied to the range of s that the step before
+ * left (a single step takes any coefficients); eps >= 0. */
 int fsdp_orthogonalize(int64_t rows, int64_t cols, int dt, const void* x, int64_t x_stride, int steps, double a,
                        double b, double c, double scale, double eps, void* out, int64_t out_stride, void* workspace,
                        size_t workspace_bytes, fsdp_stream_t stream);

@@ -101,3 +101,34 @@ def test_infinities_and_nan(rows, cols):
 @pytest.mark.parametrize("eps", [5e-324, 1e-300, 1e-40, 1.0, 1e300])
 def test_zeros_stay_zeros(rows, cols, eps):
     assert not bool(ortho(torch.zeros(rows, cols, device="cuda"), eps=eps).any())
+
+
+def condition(x, steps, coefficients):
+    """By how much, at most, an error of X is larger after the steps than before, both relative."""
+    a, b, c = coefficients
+    s = torch.linalg.svdvals(R.d(x) / R.d(x).norm())
+    k = torch.ones_like(s)
+    for _ in range(steps):
+        p = a * s + b * s ** 3 + c * s ** 5
+        k, s = k * (s * (a + 3 * b * s ** 2 + 5 * c * s ** 4) / p).abs(), p.abs()
+    return max(1.0, float(k.max()))
+
+
+@pytest.mark.parametrize("steps, coefficients", [(1, (256.0, 0.0, 0.0)), (2, (8.0, 0.0, 0.0)), (2, (-8.0, 0.0, 0.0)), (4, (2.0, 0.0, 0.0)), (3, (4.0, -6.0, 3.0)),
+                                                 (2, (8.28721201814563, -23.595886519098837, 17.300387312530933)), (1, (256.0, -256.0, 256.0))])
+@pytest.mark.parametrize("rows, cols", [(40, 70), (96, 200), (200, 96)])
+def test_polynomials_that_grow(rows, cols, steps, coefficients):
+    x = matrix("noise", rows, cols, F32)
+    want = R.orthogonalize(x, steps, coefficients)
+    assert R.distance(ortho(x, steps=steps, coefficients=coefficients), want) < ROUNDED + steps * 2.0 ** -11 * condition(x, steps, coefficients)
+
+
+@pytest.mark.parametrize("rows, cols", [(40, 1100), (1100, 1100), (2100, 1100)])
+def test_polynomials_that_grow_one_singular_value(rows, cols):
+    # all of A is one value, 64 before the last step
+    x = matrix("noise", rows, cols, F32, std=1e-6)
+    x[30, 40] = 1.0
+    want = R.orthogonalize(x, 2, (8.0, 0.0, 0.0))
+    assert R.distance(ortho(x, steps=2, coefficients=(8.0, 0.0, 0.0)), want) < ROUNDED + 2 * 2.0 ** -11
+    want = R.orthogonalize(x, 2, (4.0, 3.0, 1.0))
+    assert R.distance(ortho(x, steps=2, coefficients=(4.0, 3.0, 1.0)), want) < ROUNDED + 2 * 2.0 ** -11 * 25  # of a fifth power twice
