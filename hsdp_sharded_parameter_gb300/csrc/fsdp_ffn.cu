@@ -47,8 +47,10 @@ struct Store {
     struct Before {
         Raw<T> old;
     };
+    struct Once {};
     Mat out[kMaxGroup];
     int accumulate;
+    __device__ __forceinline__ Once once() const { return {}; }
     __device__ __forceinline__ T* place(int i, int64_t row, int64_t col) const {
         const Mat& o = i == 0 ? out[0] : (i == 1 ? out[1] : out[2]);
         return static_cast<T*>(o.data) + row * o.stride + col;
@@ -57,7 +59,7 @@ struct Store {
         if (accumulate) load_granule(b.old, place(i, row, col), 0, n);
     }
     __device__ __forceinline__ void operator()(int i, int, int64_t row, int64_t col, int n, const Cols& v, const Cols&, const Before& b,
-                                               Raw<uint16_t>&) const {
+                                               Once, Raw<uint16_t>&) const {
         Raw<T> r;
         round_to(accumulate ? v + widened(b.old) : v, r);
         store_granule(place(i, row, col), r, n);
@@ -68,11 +70,13 @@ struct Store {
 struct Gated {
     static constexpr bool kMirror = false;
     struct Before {};
+    struct Once {};
     Mat h, gate, up;
     int act;
+    __device__ __forceinline__ Once once() const { return {}; }
     __device__ __forceinline__ void bring(int, int64_t, int64_t, int, Before&) const {}
     __device__ __forceinline__ void operator()(int, int, int64_t row, int64_t col, int n, const Cols& g, const Cols& u, const Before&,
-                                               Raw<uint16_t>&) const {
+                                               Once, Raw<uint16_t>&) const {
         Cols v;
 #pragma unroll
         for (int e = 0; e < 8; ++e) v.set(e, act_value(act, g.get(e)) * u.get(e));
@@ -90,14 +94,16 @@ struct GatedGrad {
     struct Before {
         Raw<uint16_t> gate, up;
     };
+    struct Once {};
     Mat gate, up, grad_gate, grad_up, h;
     int act;
+    __device__ __forceinline__ Once once() const { return {}; }
     __device__ __forceinline__ void bring(int, int64_t row, int64_t col, int n, Before& b) const {
         load_granule(b.gate, at(gate, row, col), 0, n);
         load_granule(b.up, at(up, row, col), 0, n);
     }
     __device__ __forceinline__ void operator()(int, int, int64_t row, int64_t col, int n, const Cols& d, const Cols&, const Before& b,
-                                               Raw<uint16_t>&) const {
+                                               Once, Raw<uint16_t>&) const {
         const Cols g = widened(b.gate), u = widened(b.up);
         Cols dg, du, v;
 #pragma unroll

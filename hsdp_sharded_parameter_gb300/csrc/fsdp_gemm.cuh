@@ -1,6 +1,8 @@
 // Products of 16-bit matrices on the tensor cores, D = sum of A B^T in
-// binary32, with what becomes of D's elements left to the caller (an
-// epilogue). Included by the operators that need one.
+// binary32, with what becomes of D's elements left to the caller (an epilogue:
+// `once`, what a thread works out before its first tile; `bring`, what it loads
+// while a granule's sums are under way; and the call on the sums). Included by
+// the operators that need one.
 //
 // A pair of SMs (a cluster of two blocks) computes tiles of 256 x kN, one
 // after the other: each block brings its 128 rows of A and its half of B's kN
@@ -354,6 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     } else if (warp >= 4) {
         // takes the sums
         const int quarter = warp % 4;
+        const typename Epi::Once once = epi.once();
         float* stage = stages + (warp - 4) * (kStageRoom / 4);
         int n_done = 0;
         for (int item = pair; item < items; item += pairs, ++n_done) {
@@ -398,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int64_t row = row0 + 8 * i + lane / 4;
-                    if (row < m && cols > 0) epi(p.product, split, row, col, cols, x[i], y[i], before[i], r[i]);
+                    if (row < m && cols > 0) epi(p.product, split, row, col, cols, x[i], y[i], before[i], once, r[i]);
                 }
                 if constexpr (Epi::kMirror) {
                     if (mirror) {
@@ -443,12 +446,14 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 struct Parts {
     static constexpr bool kMirror = false;
     struct Before {};
+    struct Once {};
     float* sums;
     int64_t m, ld;
     int planes;
+    __device__ __forceinline__ Once once() const { return {}; }
     __device__ __forceinline__ void bring(int, int64_t, int64_t, int, Before&) const {}
     __device__ __forceinline__ void operator()(int, int split, int64_t row, int64_t col, int, const Cols& x, const Cols& y, const Before&,
-                                               Raw<uint16_t>&) const {
+                                               Once, Raw<uint16_t>&) const {
         // ld is whole granules: the columns past n are sums of zeros
         float4* p = reinterpret_cast<float4*>(sums + ((int64_t)split * planes * m + row) * ld + col);
         p[0] = make_float4(x.p[0].x, x.p[0].y, x.p[1].x, x.p[1].y);
@@ -467,6 +472,7 @@ __global__ void __launch_bounds__(256) join_kernel(const float* sums, int splits
     allow_next();
     wait_for_previous();
     const int64_t per = (n + kGran - 1) / kGran, granules = m * per;
+    const typename Epi::Once once = epi.once();
     for (int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x; g < granules; g += (int64_t)gridDim.x * 256) {
         const int64_t row = g / per, col = (g - row * per) * kGran;
         const int cols = n - col < kGran ? (int)(n - col) : kGran;
@@ -482,7 +488,7 @@ __global__ void __launch_bounds__(256) join_kernel(const float* sums, int splits
             }
         }
         Raw<uint16_t> r;
-        epi(0, 0, row, col, cols, x, y, before, r);
+        epi(0, 0, row, col, cols, x, y, before, once, r);
     }
 }
 

@@ -102,12 +102,22 @@ __global__ void __launch_bounds__(kSquareThreads) square_kernel(Mat x, int64_t r
     }
 }
 
-// lift / (|x| + eps) from the parts, as a product of two factors neither of
-// which leaves binary32's range. All threads of a block of at least 96 take
-// part.
-__device__ __forceinline__ float2 norm_factor(const double* parts, double eps, float lift) {
+// What x is multiplied by on its way into X, as a product of two factors neither
+// of which leaves binary32's range, and the power of two by which X is then above
+// x / (|x| + eps).
+struct Factor {
+    float first, second;
+    int lift;
+    __device__ __forceinline__ float of(float v) const { return v * first * second; }
+    __device__ __forceinline__ Cols of(const Cols& v) const { return v * all(first) * all(second); }
+};
+
+// 2^sx 2^e / (|x| + eps) from the parts. Where `full`, e brings X to a norm
+// between 1/4 and 1 if it is below; else e is 0. All threads of a block of at
+// least 96 take part.
+__device__ __forceinline__ Factor norm_factor(const double* parts, double eps, int sx, bool full) {
     __shared__ double sums[3];
-    __shared__ float2 factor;
+    __shared__ Factor factor;
     if (threadIdx.x < 96) {
         double s = 0.0;
         for (int i = threadIdx.x % 32; i < kSquareBlocks; i += 32) s += parts[threadIdx.x / 32 * kSquareBlocks + i];
@@ -118,33 +128,48 @@ __device__ __forceinline__ float2 norm_factor(const double* parts, double eps, f
     __syncthreads();
     if (threadIdx.x == 0) {
         const double norm = sqrt(sums[0] * 0x1p-180 + sums[1] + sums[2] * 0x1p180);
+        const int lift = full && norm > 0.0 && isfinite(norm) ? max(0, ilogb(norm + eps) - ilogb(norm) - 1) : 0;
         // a norm is 0 or at least 2^-149: a quotient above 2^165 has only zeros to scale (without an eps it is 0 / 0)
-        double f = (double)lift / (norm + eps);
+        double f = ldexp(1.0 / (norm + eps), sx + lift);
         if (norm + eps > 0.0) f = fmin(f, 0x1p200);
         int e = 0;
         const double m = frexp(f, &e);
-        factor = isfinite(f) ? make_float2(ldexpf(1.0f, e / 2), (float)ldexp(m, e - e / 2)) : make_float2((float)f, 1.0f);
+        factor = isfinite(f) ? Factor{ldexpf(1.0f, e / 2), (float)ldexp(m, e - e / 2), lift} : Factor{(float)f, 1.0f, lift};
     }
     __syncthreads();
     return factor;
 }
 
-// X = x / (|x| + eps) as two planes scaled by `lift`.
+// X = x / (|x| + eps) as two planes scaled by 2^sx, and by what `lift` receives.
+// (Without that, where eps is far above |x|, all of X would lie below what the
+// planes resolve: half of it was gone at eps = 10^7 |x|.)
 template <typename T>
-__global__ void __launch_bounds__(256) planes_kernel(Mat x, int64_t rows, int64_t cols, const double* parts, double eps, float lift, Mat hi,
-                                                     Mat lo) {
+__global__ void __launch_bounds__(256) planes_kernel(Mat x, int64_t rows, int64_t cols, const double* parts, double eps, int sx, Mat hi, Mat lo,
+                                                     int* lift) {
     wait_for_previous();
-    const float2 f = norm_factor(parts, eps, lift);
+    const Factor f = norm_factor(parts, eps, sx, true);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *lift = f.lift;
     const int64_t per = (cols + kGran - 1) / kGran, all_granules = rows * per;
     for (int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x; g < all_granules; g += (int64_t)gridDim.x * 256) {
         const int64_t row = g / per, i = g - row * per;
         const int n = granule_cols(i, cols);
         Raw<T> r;
         load_granule(r, static_cast<const T*>(x.data) + row * x.stride, i * kGran, n);
-        put_planes(hi, lo, row, i * kGran, n, widened(r) * all(f.x) * all(f.y));
+        put_planes(hi, lo, row, i * kGran, n, f.of(widened(r)));
     }
 }
 
+// The power of two e by which a step's X is above the iteration's: what
+// planes_kernel began with, less what the steps may have grown by since. With
+// g_t for the most that step t multiplies a singular value by, in powers of two
+// rounded up, e becomes max(0, e - g_t), so no singular value leaves the range;
+// in closed form over the steps, max(first - less, least). (Looked up once a
+// thread: once a granule 4096 x 11008 took 2.63 ms instead of 2.35.)
+struct Lift {
+    const int* first;
+    int less, least;
+    __device__ __forceinline__ int now() const { return max(*first - less, least); }
+};
 // ------------------------------------------------------ one short side
 //
 // With at most 64 rows (or columns) X stays in binary32, in blocks of 64 of its
@@ -201,7 +226,7 @@ __global__ void __launch_bounds__(kNarrowThreads) narrow_first_kernel(Mat x, int
                                                                       float* shares) {
     __shared__ __align__(16) float columns[kChunk * kSidePitch];
     wait_for_previous();
-    const float2 f = norm_factor(parts, eps, 1.0f);
+    const Factor f = norm_factor(parts, eps, 0, false);
     const T* data = static_cast<const T*>(x.data);
     const int i0 = threadIdx.x / 16 * 4, j0 = threadIdx.x % 16 * 4;
     GramShare share;
@@ -210,7 +235,7 @@ __global__ void __launch_bounds__(kNarrowThreads) narrow_first_kernel(Mat x, int
         for (int c = threadIdx.x; c < kSide * kChunk; c += kNarrowThreads) {
             const int i = tall ? c % kSide : c / kChunk, j = tall ? c / kSide : c % kChunk;
             float v = 0.0f;
-            if (i < p && first + j < q) v = value_of(tall ? data + (first + j) * x.stride + i : data + i * x.stride + first + j) * f.x * f.y;
+            if (i < p && first + j < q) v = f.of(value_of(tall ? data + (first + j) * x.stride + i : data + i * x.stride + first + j));
             columns[j * kSidePitch + i] = v;
         }
         __syncthreads();
@@ -299,30 +324,40 @@ __global__ void __launch_bounds__(kNarrowThreads) narrow_step_kernel(float* held
 struct Gram {
     static constexpr bool kMirror = true;
     struct Before {};
+    struct Once {};
     Mat out;
     float scale;
+    __device__ __forceinline__ Once once() const { return {}; }
     __device__ __forceinline__ void bring(int, int64_t, int64_t, int, Before&) const {}
     __device__ __forceinline__ void put(int64_t row, int64_t col, int n, const Raw<uint16_t>& r) const { store_granule(at(out, row, col), r, n); }
     __device__ __forceinline__ void operator()(int, int, int64_t row, int64_t col, int n, const Cols& v, const Cols&, const Before&,
-                                               Raw<uint16_t>& r) const {
+                                               Once, Raw<uint16_t>& r) const {
         round_half(v * all(scale), r);
         put(row, col, n, r);
     }
 };
 
-// c A A + b A + d I.
+// c A A + b A + d I, of an A that is 2^(2 e) of what it stands for.
 struct Poly {
     static constexpr bool kMirror = true;
     struct Before {
         Raw<uint16_t> a;
     };
+    struct Once {
+        float square, linear;
+    };
     Mat a, out;
     float square, linear, diagonal;
+    Lift lift;
+    __device__ __forceinline__ Once once() const {
+        const int e = lift.now();
+        return {ldexpf(square, -4 * e), ldexpf(linear, -2 * e)};
+    }
     __device__ __forceinline__ void bring(int, int64_t row, int64_t col, int n, Before& b) const { load_granule(b.a, at(a, row, col), 0, n); }
     __device__ __forceinline__ void put(int64_t row, int64_t col, int n, const Raw<uint16_t>& r) const { store_granule(at(out, row, col), r, n); }
-    __device__ __forceinline__ void operator()(int, int, int64_t row, int64_t col, int n, const Cols& v, const Cols&, const Before& b,
+    __device__ __forceinline__ void operator()(int, int, int64_t row, int64_t col, int n, const Cols& v, const Cols&, const Before& b, Once by,
                                                Raw<uint16_t>& r) const {
-        Cols s = fma(v, all(square), widened_half(b.a) * all(linear));
+        Cols s = fma(v, all(by.square), widened_half(b.a) * all(by.linear));
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             if (col + e == row) s.set(e, s.get(e) + diagonal);
@@ -337,16 +372,24 @@ struct Next {
     struct Before {
         Raw<uint16_t> hi, lo;
     };
+    struct Once {
+        float scale, shift;
+    };
     Mat hi, lo, next, out;  // out.data: the caller's
     float scale, shift;
+    Lift lift, after;  // X's, and that of the next
+    __device__ __forceinline__ Once once() const {
+        const int e = (out.data ? 0 : after.now()) - lift.now();
+        return {ldexpf(scale, e), ldexpf(shift, e)};
+    }
     __device__ __forceinline__ void bring(int, int64_t row, int64_t col, int n, Before& b) const {
         load_granule(b.hi, at(hi, row, col), 0, n);
         load_granule(b.lo, at(lo, row, col), 0, n);
     }
-    __device__ __forceinline__ void operator()(int, int, int64_t row, int64_t col, int n, const Cols& v, const Cols&, const Before& b,
+    __device__ __forceinline__ void operator()(int, int, int64_t row, int64_t col, int n, const Cols& v, const Cols&, const Before& b, Once by,
                                                Raw<uint16_t>& r) const {
         Cols x = fma(widened_half(b.lo), all(1.0f / kLow), widened_half(b.hi));
-        x = fma(v, all(scale), x * all(shift));
+        x = fma(v, all(by.scale), x * all(by.shift));
         if (!out.data) {
             put_planes(next, lo, row, col, n, x);
         } else {
@@ -356,7 +399,7 @@ struct Next {
     }
 };
 
-constexpr size_t kPartsRoom = (3 * kSquareBlocks * 8 + 255) / 256 * 256;
+constexpr size_t kPartsRoom = ((3 * kSquareBlocks + 1) * 8 + 255) / 256 * 256;  // and the first lift
 
 // Blocks of columns, shares of A, and their room with A and X.
 int64_t narrow_blocks(int64_t q) { return (q + kChunk - 1) / kChunk; }
@@ -417,21 +460,40 @@ size_t ortho_bytes(int64_t rows, int64_t cols) {
     return kPartsRoom + 3 * aligned_room(rows, cols) + 2 * aligned_room(p, p) + sums_bytes(rows, cols);
 }
 
-double ortho_reach(int steps, double a, double b, double c) {
-    double reach = 1.0;
-    for (int t = 1; t < steps && reach <= kMostReach * 2; ++t) {
-        // the most of |a s + b s^3 + c s^5| for s in [0, reach]: at its end or where the derivative, a polynomial of s^2, is 0
-        const double u = reach * reach, root = 9.0 * b * b - 20.0 * a * c;
-        double at[3] = {u, 0.0, 0.0};
-        if (root >= 0.0) {
-            const double half = -0.5 * (3.0 * b + std::copysign(std::sqrt(root), b));
-            if (c != 0.0) at[1] = half / (5.0 * c);
-            if (half != 0.0) at[2] = a / half;
-        }
-        for (const double v : at)
-            if (v > 0.0 && v <= u) reach = std::max(reach, std::fabs(std::sqrt(v) * (a + b * v + c * v * v)));
+namespace {
+// What a step does to singular values from [0, s]: the most of |a s + b s^3 + c
+// s^5|, and of that over s.
+struct Reach {
+    double value, growth;
+};
+Reach reach_of(double s, double a, double b, double c) {
+    const double u = s * s, root = 9.0 * b * b - 20.0 * a * c;
+    // of u = s^2: the range's end, and where the derivatives a + 3 b u + 5 c u^2 and b + 2 c u are 0
+    double at[4] = {u, 0.0, 0.0, 0.0};
+    if (root >= 0.0) {
+        const double half = -0.5 * (3.0 * b + std::copysign(std::sqrt(root), b));
+        if (c != 0.0) at[1] = half / (5.0 * c);
+        if (half != 0.0) at[2] = a / half;
     }
-    return reach;
+    if (c != 0.0) at[3] = -b / (2.0 * c);
+    Reach r = {0.0, std::fabs(a)};
+    for (const double v : at) {
+        if (!(v > 0.0 && v <= u)) continue;
+        const double growth = std::fabs(a + b * v + c * v * v);
+        r.value = std::max(r.value, std::sqrt(v) * growth);
+        r.growth = std::max(r.growth, growth);
+    }
+    return r;
+}
+}  // namespace
+
+double ortho_reach(int steps, double a, double b, double c) {
+    double most = 1.0, s = 1.0;
+    for (int t = 1; t < steps && most <= 2 * kMostReach; ++t) {
+        s = reach_of(s, a, b, c).value;
+        most = std::max(most, s);
+    }
+    return most;
 }
 
 cudaError_t launch_ortho(int dt, const OrthoArgs& a, cudaStream_t s) {
@@ -455,7 +517,7 @@ cudaError_t launch_ortho(int dt, const OrthoArgs& a, cudaStream_t s) {
     const int sa = std::min({13, log2_near((double)p), 15 - log2_above(square)});
     const double most = std::fabs(a.a) + square * std::fabs(a.b) + square * square * std::fabs(a.c);
     const int sb = std::min(sa, 15 - log2_above(std::max(most, 1.0)));
-    const float lift = std::ldexp(1.0f, sx);
+    int* first_lift = reinterpret_cast<int*>(parts + 3 * kSquareBlocks);
     if (dt == FSDP_F32)
         square_kernel<float><<<kSquareBlocks, kSquareThreads, 0, s>>>(a.x, a.rows, a.cols, parts);
     else
@@ -466,19 +528,26 @@ cudaError_t launch_ortho(int dt, const OrthoArgs& a, cudaStream_t s) {
     if (p <= kSide) return dt == FSDP_F32 ? narrow<float>(a, s) : narrow<uint16_t>(a, s);
     const int64_t granules = a.rows * ((a.cols + kGran - 1) / kGran);
     const int grid = (int)std::min<int64_t>((granules + 255) / 256, 8 * sm_count());
-    e = dt == FSDP_F32 ? launch_next(planes_kernel<float>, dim3(grid), 256, 0, s, a.x, a.rows, a.cols, (const double*)parts, a.eps, lift, hi, lo)
-                       : launch_next(planes_kernel<uint16_t>, dim3(grid), 256, 0, s, a.x, a.rows, a.cols, (const double*)parts, a.eps, lift, hi, lo);
+    e = dt == FSDP_F32 ? launch_next(planes_kernel<float>, dim3(grid), 256, 0, s, a.x, a.rows, a.cols, (const double*)parts, a.eps, sx, hi, lo, first_lift)
+                       : launch_next(planes_kernel<uint16_t>, dim3(grid), 256, 0, s, a.x, a.rows, a.cols, (const double*)parts, a.eps, sx, hi, lo, first_lift);
     count_launch();
+    double from = 1.0;
+    Lift lift = {first_lift, 0, 0};
     for (int i = 0; i < a.steps && e == cudaSuccess; ++i) {
         const float shift = i + 2 < a.steps ? a.a : 0.5f * (1.0f + a.a);
         e = launch_product(gram_product(p, q, tall, hi), Gram{gram, std::ldexp(1.0f, sa - 2 * sx)}, sums, s, false);
-        const Poly mix = {gram, poly, std::ldexp(a.c, sb - 2 * sa), std::ldexp(a.b, sb - sa), std::ldexp(a.a - shift, sb)};
+        const Poly mix = {gram, poly, std::ldexp(a.c, sb - 2 * sa), std::ldexp(a.b, sb - sa), std::ldexp(a.a - shift, sb), lift};
         if (e == cudaSuccess) e = launch_product(square_product(p, gram), mix, sums, s, false);
         const bool last = i + 1 == a.steps;
         const float out = last ? std::ldexp(a.scale, -sx) : 1.0f;
+        const Reach step = reach_of(from, a.a, a.b, a.c);
+        const int grown = std::max(-16, log2_above(std::max(step.growth, 0x1p-20)));
+        const Lift after = {first_lift, lift.less + grown, std::max(0, lift.least - grown)};
         if (e == cudaSuccess)
             e = launch_product(next_product(a.rows, a.cols, poly, hi),
-                               Next{hi, lo, next, last ? a.out : Mat{nullptr, 0}, std::ldexp(out, -sb), shift * out}, sums, s, false);
+                               Next{hi, lo, next, last ? a.out : Mat{nullptr, 0}, std::ldexp(out, -sb), shift * out, lift, after}, sums, s, false);
+        lift = after;
+        from = step.value;
         std::swap(hi, next);
     }
     return e;

@@ -576,9 +576,9 @@ int fsdp_orthogonalize_workspace(int64_t rows, int64_t cols, size_t* bytes);
  * and out = scale * X. With the coefficients (3.4445, -4.7750, 2.0315) five
  * steps bring x's larger singular values to between about 0.7 and 1.2. x has
  * type dt, out is bfloat16. Where x has more than 64 rows and columns, X is held
- * in 22 bits and A and the polynomial in binary16 under a power of two, and up
- * to a dozen steps put out off by up to 2^-11 each, in the 2-norm, beside its own
- * rounding (five steps 0.0020 in all on noise, twelve 0.0046); else everything
+ * in 22 bits and A and the polynomial in binary16, all three under powers of
+ * two that follow x, eps and the coefficients, and up to a dozen steps (of |a|
+ * >= 1) put out off by up to 2^-11 each, in the 2-norm, beside its own rounding (five steps 0.0020 in all on noise, twelve 0.0046); else everything
  * is in binary32. Directions in which x has next to nothing hold what rounding
  * left there, as they do in any arithmetic, and the steps lift that as they lift
  * anything, by up to |a| each: with these coefficients 2^-22 of |x| is 2^-13

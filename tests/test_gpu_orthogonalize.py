@@ -132,3 +132,15 @@ def test_polynomials_that_grow_one_singular_value(rows, cols):
     assert R.distance(ortho(x, steps=2, coefficients=(8.0, 0.0, 0.0)), want) < ROUNDED + 2 * 2.0 ** -11
     want = R.orthogonalize(x, 2, (4.0, 3.0, 1.0))
     assert R.distance(ortho(x, steps=2, coefficients=(4.0, 3.0, 1.0)), want) < ROUNDED + 2 * 2.0 ** -11 * 25  # of a fifth power twice
+
+
+@pytest.mark.parametrize("steps, coefficients", [(1, DEFAULT), (5, DEFAULT), (40, QUINTIC), (3, (1.0, 0.0, 0.0)), (3, (0.25, 0.0, 0.0)), (2, (8.0, 0.0, 0.0))])
+@pytest.mark.parametrize("rows, cols", [(40, 70), (100, 130), (1030, 520)])
+@pytest.mark.parametrize("kind", ["noise", "spikes"])
+def test_eps_far_above_the_norm(rows, cols, kind, steps, coefficients):
+    # X_0 is x over eps, and small: what the steps leave of it is as exact as ever
+    x = matrix(kind, rows, cols, F32)
+    norm = float(R.d(x).norm())
+    for ratio in (1e-2, 1.0, 1e2, 1e4, 1e7, 1e10, 1e15, 1e25):
+        k = dict(steps=steps, coefficients=coefficients, eps=norm * ratio, scale=2.0)
+        assert R.distance(ortho(x, **k), R.orthogonalize(x, **k)) < ROUNDED + steps * 2.0 ** -11, ratio

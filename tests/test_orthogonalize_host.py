@@ -18,10 +18,11 @@ def call(steps, a, b, c, rows=70, cols=90):
 
 def reach(steps, a, b, c):
     """The largest singular value that a step starts from, on a grid."""
-    most = 1.0
+    most = top = 1.0
     for _ in range(steps - 1):
-        s = np.linspace(0, most, 20001)
-        most = max(most, float(np.abs(a * s + b * s ** 3 + c * s ** 5).max()))
+        s = np.linspace(0, top, 20001)
+        top = float(np.abs(a * s + b * s ** 3 + c * s ** 5).max())
+        most = max(most, top)
         if most > 1e6:
             break
     return most
@@ -29,7 +30,7 @@ def reach(steps, a, b, c):
 
 CASES = [(1, 256, 0, 0), (2, 256, 0, 0), (2, 8, 0, 0), (2, -8, 0, 0), (2, 8.01, 0, 0), (4, 2, 0, 0), (5, 2, 0, 0), (64, 1, 0, 0), (3, 0, -2.8, 0),
          (5, 4, -6, 3), (3, 4, -6, 3), (64, 3.4445, -4.7750, 2.0315), (64, 1.875, -1.25, 0.375), (64, 1.5, -0.5, 0), (64, 2, -1.5, 0.5),
-         (64, 0, 0, 0), (64, 256, -256, 0), (2, 256, -256, 256), (1, 256, -256, 256), (64, -1, 0, 0), (9, 1.25, 0, 0), (11, 1.25, 0, 0),
+         (64, 0, 0, 0), (64, 256, -256, 0), (2, 256, -256, 256), (1, 256, -256, 256), (64, -1, 0, 0), (64, 0.5, 0.25, -0.1), (9, 1.25, 0, 0), (11, 1.25, 0, 0),
          (2, 8.28721201814563, -23.595886519098837, 17.300387312530933), (3, 8.28721201814563, -23.595886519098837, 17.300387312530933)]
 
 
