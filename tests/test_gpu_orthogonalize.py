@@ -18,6 +18,7 @@ import pytest
 import torch
 
 import products_ref as R
+from hsdp_sharded_parameter_gb300 import capi as C
 from test_gpu_products import BF16, F32, matrix, no_wait_ran_out, ortho  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -144,3 +145,20 @@ def test_eps_far_above_the_norm(rows, cols, kind, steps, coefficients):
     for ratio in (1e-2, 1.0, 1e2, 1e4, 1e7, 1e10, 1e15, 1e25):
         k = dict(steps=steps, coefficients=coefficients, eps=norm * ratio, scale=2.0)
         assert R.distance(ortho(x, **k), R.orthogonalize(x, **k)) < ROUNDED + steps * 2.0 ** -11, ratio
+
+
+@pytest.mark.parametrize("shape", [(1, 30000001), (50000017, 1), (1, 1 << 25), (2, 10 ** 7)], ids=str)
+def test_long_rows(shape):
+    # a + b A leaves 1/16 of X, so an error of A shows 31 times as large. A's sum over a row is in stretches of at
+    # most 2048 additions, and of less than 64 stretches a part at these lengths, so where all roundings go the
+    # same way A is off by 2112 * 2^-24 at most.
+    x = torch.ones(shape, device="cuda")
+    if min(shape) > 1:
+        x[1] = torch.randn(shape[1], generator=torch.Generator(device="cuda").manual_seed(1), device="cuda") * 1e-6
+    work = torch.empty(C.fsdp_orthogonalize_workspace(*shape), dtype=torch.uint8, device="cuda")
+    out = torch.empty(shape, dtype=BF16, device="cuda")
+    C.fsdp_orthogonalize(x, out, work, steps=1, coefficients=(2.0, -1.9375, 0.0))
+    want = R.orthogonalize(x, 1, (2.0, -1.9375, 0.0))
+    # the same rounding in all places, so no mean over places helps: half a step of bfloat16, which has 8 bits,
+    # is 2^-8 of a value just above a power of two (1.1411e-5 = 191.45 steps of 2^-24 becomes 191 of them)
+    assert R.distance(out, want) < 2.0 ** -8 + 31 * 2112 * 2.0 ** -24
