@@ -11,9 +11,12 @@ __device__ __forceinline__ uint16_t* at(const Mat& m, int64_t row, int64_t col) 
 // ------------------------------------------------------------- activations
 
 __device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.0f, 1.0f + expf(-z)); }
+// The normal distribution's integral up to z. (As (1 + erf) / 2 it has no digits
+// left below z = -5.)
+__device__ __forceinline__ float normal_below(float z) { return 0.5f * erfcf(z * -0.70710678118654752f); }
 __device__ __forceinline__ float act_value(int act, float z) {
     if (act == FSDP_SILU) return z * sigmoid(z);
-    if (act == FSDP_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+    if (act == FSDP_GELU) return z * normal_below(z);
     return z <= 0.0f ? 0.0f : z;
 }
 // The value, and the derivative in `slope`.
@@ -24,7 +27,7 @@ __device__ __forceinline__ float act_both(int act, float z, float& slope) {
         return v;
     }
     if (act == FSDP_GELU) {
-        const float p = 0.5f + 0.5f * erff(z * 0.70710678118654752f);
+        const float p = normal_below(z);
         slope = __fmaf_rn(z * 0.39894228040143268f, expf(-0.5f * z * z), p);
         return z * p;
     }
