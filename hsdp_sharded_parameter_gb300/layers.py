@@ -163,9 +163,20 @@ class GatedBlock:
         self.unit.reduce_grads_one_pass(op)
         return self.grad_x
 
+    def check_status(self):
+        """Raises if a wait inside a kernel of the block's operators has run out
+        since the last question: what they gave is undefined then. Synchronises
+        the current stream."""
+        if C.fsdp_operators_status():
+            raise RuntimeError("gated block: a wait inside a kernel of its operators ran out")
+
     def step(self, lr, mu=0.95):
         """Momentum, orthogonalised, onto the shards: scaled by
-        sqrt(max(1, rows / cols))."""
+        sqrt(max(1, rows / cols)). Asks check_status before the gradients go into
+        the momentum and before an update goes onto the shards, but not while
+        the stream is captured: a graph's user asks after the replay."""
+        check = (lambda: None) if torch.cuda.is_current_stream_capturing() else self.check_status
+        check()
         for q, (rows, cols) in enumerate(self.shapes):
             m = self.momentum[q].mul_(mu)
             spans = [self.plan.sharded_size(q, s) for s in range(self.plan.S)]
@@ -173,6 +184,7 @@ class GatedBlock:
                 m[first:first + n].add_(self.unit.shard_grads[s * self.plan.P + q].view(n, cols))
             update = torch.empty(rows, cols, dtype=torch.bfloat16, device=m.device)
             C.fsdp_orthogonalize(m, update, self.work, scale=math.sqrt(max(1.0, rows / cols)))
+            check()
             for w in range(self.plan.W):
                 first, n = spans[w % self.plan.S]
                 self.unit.shards[w * self.plan.P + q].view(n, cols).add_(update[first:first + n], alpha=-lr)
