@@ -609,6 +609,15 @@ def fsdp_operators_status(stream=None):
     return v.value
 
 
+def _whole(what, bits, **numbers):
+    """Numbers that the C ABI's types would cut, and stand for others then, are refused."""
+    for name, n in numbers.items():
+        if not hasattr(n, "__index__"):
+            _refuse(what, f"{name} {n!r} is no whole number")
+        if not -(1 << bits - 1) <= n < 1 << bits - 1:
+            _refuse(what, f"{name} {n} does not fit {bits} bits")
+
+
 def _aligned(hidden, inner, aligned):
     return int(hidden % 8 == 0 and inner % 8 == 0) if aligned is None else int(bool(aligned))
 
@@ -618,14 +627,15 @@ def fsdp_gated_ffn_workspace(tokens, hidden, inner, aligned=None):
     fewer. aligned: whether the rows of all its matrices start on the 16-byte
     grid, as contiguous ones do where hidden and inner are multiples of 8 (the
     default: whether they are)."""
+    _whole("gated_ffn_workspace", 64, tokens=tokens, hidden=hidden, inner=inner)
     b = ctypes.c_size_t()
     _check(lib().fsdp_gated_ffn_workspace(tokens, hidden, inner, _aligned(hidden, inner, aligned), ctypes.byref(b)))
     return b.value
 
 
 def _activation(what, name):
-    act = ACTIVATIONS.get(name, name)
-    if not isinstance(act, int):
+    act = ACTIVATIONS.get(name) if isinstance(name, str) else name
+    if isinstance(act, bool) or not isinstance(act, int) or act not in ACTIVATIONS.values():
         _refuse(what, f"activation {name!r} is none of {sorted(ACTIVATIONS)}")
     return act
 
@@ -637,6 +647,7 @@ def fsdp_gated_ffn(x, w_gate, w_up, w_down, out, workspace, activation="silu", g
     gradient needs. activation: "silu", "gelu" or "relu". workspace: a tensor of
     at least fsdp_gated_ffn_workspace(tokens, hidden, inner) bytes."""
     what = "gated_ffn"
+    act = _activation(what, activation)
     xp, rows, cols, xs, dt, dev = _matrix(what, "x", x)
     if dt != FSDP_BF16:
         _refuse(what, f"x is {x.dtype}; expected bfloat16")
@@ -649,7 +660,6 @@ def fsdp_gated_ffn(x, w_gate, w_up, w_down, out, workspace, activation="silu", g
     if (gate is None) != (up is None):
         _refuse(what, "gate and up: one of them is None")
     op, os_ = _like(what, "out", out, rows, cols, dt, dev)
-    act = _activation(what, activation)
     wp, wb = _work(what, workspace, dev)
     handle = _on(what, dev, stream)
     _check(lib().fsdp_gated_ffn(rows, cols, inner, xp, xs, gp, gs, up_, us, dp, ds, act, kg, kgs, ku, kus, op, os_, wp, wb,
@@ -658,6 +668,7 @@ def fsdp_gated_ffn(x, w_gate, w_up, w_down, out, workspace, activation="silu", g
 
 def fsdp_gated_ffn_grad_workspace(tokens, hidden, inner, aligned=None):
     """Bytes of the workspace that fsdp_gated_ffn_grad needs, as fsdp_gated_ffn_workspace."""
+    _whole("gated_ffn_grad_workspace", 64, tokens=tokens, hidden=hidden, inner=inner)
     b = ctypes.c_size_t()
     _check(lib().fsdp_gated_ffn_grad_workspace(tokens, hidden, inner, _aligned(hidden, inner, aligned), ctypes.byref(b)))
     return b.value
@@ -670,6 +681,7 @@ def fsdp_gated_ffn_grad(grad_out, x, w_gate, w_up, w_down, gate, up, grad_x, gra
     what they hold). workspace: a tensor of at least
     fsdp_gated_ffn_grad_workspace(tokens, hidden, inner) bytes."""
     what = "gated_ffn_grad"
+    act = _activation(what, activation)
     gp, rows, cols, gs, dt, dev = _matrix(what, "grad_out", grad_out)
     if dt != FSDP_BF16:
         _refuse(what, f"grad_out is {grad_out.dtype}; expected bfloat16")
@@ -685,7 +697,6 @@ def fsdp_gated_ffn_grad(grad_out, x, w_gate, w_up, w_down, gate, up, grad_x, gra
     dgp, dgs = _like(what, "grad_w_gate", grad_w_gate, inner, cols, pdt, dev)
     dup, dus = _like(what, "grad_w_up", grad_w_up, inner, cols, pdt, dev)
     ddp, dds = _like(what, "grad_w_down", grad_w_down, cols, inner, pdt, dev)
-    act = _activation(what, activation)
     wp, wb = _work(what, workspace, dev)
     handle = _on(what, dev, stream)
     _check(lib().fsdp_gated_ffn_grad(rows, cols, inner, gp, gs, xp, xs, wgp, wgs, wup, wus, wdp, wds, kg, kgs, ku, kus, act, dxp,
@@ -694,6 +705,7 @@ def fsdp_gated_ffn_grad(grad_out, x, w_gate, w_up, w_down, gate, up, grad_x, gra
 
 def fsdp_orthogonalize_workspace(rows, cols):
     """Bytes of the workspace that fsdp_orthogonalize needs."""
+    _whole("orthogonalize_workspace", 64, rows=rows, cols=cols)
     b = ctypes.c_size_t()
     _check(lib().fsdp_orthogonalize_workspace(rows, cols, ctypes.byref(b)))
     return b.value
@@ -707,6 +719,7 @@ def fsdp_orthogonalize(x, out, workspace, steps=5, coefficients=(3.4445, -4.7750
     workspace: a tensor of at least fsdp_orthogonalize_workspace(rows, cols)
     bytes."""
     what = "orthogonalize"
+    _whole(what, 32, steps=steps)
     xp, rows, cols, xs, dt, dev = _matrix(what, "x", x)
     op, os_ = _like(what, "out", out, rows, cols, FSDP_BF16, dev)
     a, b, c = coefficients
