@@ -307,16 +307,17 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                     if (++stage == kStg) stage = 0, phase ^= 1;
                 }
             }
-            if (!ok) {
-                // given up: what is on its way here has to arrive before the
-                // block ends. The first block sees it on its barriers; the
-                // second's copies count there too, so it gives them time.
-                if (rank == 0) {
-                    for (int i = 0; i < kStg && i < brought; ++i) {
-                        const int at = (brought - 1 - i) % kStg;
-                        bar_wait(&full[at], (uint32_t)((brought - 1 - i) / kStg & 1));
-                    }
-                } else {
+            // What is on its way here has to arrive before the block ends. The
+            // first block sees it on its barriers. The second's copies count
+            // there too: it waits until its last stages have been read, and
+            // where that does not come, for a time in which copies do.
+            const int last = min(brought, kStg);
+            if (rank == 0) {
+                for (int j = brought - 1; j >= brought - last; --j)
+                    if (!bar_wait(&full[j % kStg], (uint32_t)(j / kStg & 1))) break;
+            } else {
+                for (int j = brought - 1; j >= brought - last && ok; --j) ok = bar_wait(&empty[j % kStg], (uint32_t)(j / kStg & 1));
+                if (!ok) {
                     const uint64_t from = clock_ns();
                     for (int i = 0; i < 100000 && clock_ns() - from < 100000000ull; ++i) __nanosleep(1000);
                 }
@@ -348,10 +349,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 }
                 if (ok) mma_commit(&done[half]);
             }
-            if (!ok) {
-                mma_commit(&drained);
-                bar_wait(&drained, 0);
-            }
+            // None of the tensor cores' work is under way when the blocks end: the
+            // takers of the last sums would see it end, but may have given up.
+            mma_commit(&drained);
+            bar_wait(&drained, 0);
         }
     } else if (warp >= 4) {
         // takes the sums
