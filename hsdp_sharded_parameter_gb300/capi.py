@@ -597,7 +597,9 @@ def fsdp_layer_norm_grad(grad_out, hidden, mean, rstd, weight, grad_x, grad_weig
 
 # ----------------------------------------- products of a feed-forward block
 #
-# Matrices are passed as above, in bfloat16 where nothing else is said.
+# Matrices are passed as above, in bfloat16 where nothing else is said. A sum has
+# up to 2^24 terms: hidden, inner and a gradient's tokens, and both sides of a
+# matrix to orthogonalise that has more than 64 rows and columns.
 
 
 def fsdp_operators_status(stream=None):

@@ -132,6 +132,23 @@ int check_product(const char* what, std::initializer_list<int64_t> sizes) {
     return FSDP_OK;
 }
 
+// A tile's sum over k runs in one go, in binary32, and the warps that wait for it
+// wait two seconds: 2^24 terms, two products of which are added at most, take
+// 0.4 s where all SMs share the memory.
+constexpr int64_t kMostTerms = (int64_t)1 << 24;
+
+int check_terms(const char* what, std::initializer_list<int64_t> lengths) {
+    for (const int64_t n : lengths)
+        if (n > kMostTerms) return bad(what, "a sum of more than 2^24 terms");
+    return FSDP_OK;
+}
+
+// X is summed over its longer side where the other has more than 64.
+int check_ortho_size(const char* what, int64_t rows, int64_t cols) {
+    if (int rc = check_product(what, {rows, cols})) return rc;
+    return rows > 64 && cols > 64 ? check_terms(what, {rows, cols}) : FSDP_OK;
+}
+
 int check_activation(const char* what, int act) {
     return act == FSDP_SILU || act == FSDP_GELU || act == FSDP_RELU ? FSDP_OK : bad(what, "unknown activation");
 }
@@ -303,6 +320,7 @@ int fsdp_gated_ffn_workspace(int64_t tokens, int64_t hidden, int64_t inner, int 
     clear_error();
     if (!bytes) return bad(what, "bytes is NULL");
     FSDP_TRY(check_product(what, {tokens, hidden, inner}));
+    FSDP_TRY(check_terms(what, {hidden, inner}));
     *bytes = ffn_most_bytes(tokens, hidden, inner, aligned != 0);
     return FSDP_OK;
 }
@@ -315,6 +333,7 @@ int fsdp_gated_ffn(int64_t tokens, int64_t hidden, int64_t inner, const void* x,
     const char* what = "gated_ffn";
     clear_error();
     FSDP_TRY(check_product(what, {tokens, hidden, inner}));
+    FSDP_TRY(check_terms(what, {hidden, inner}));
     FSDP_TRY(check_activation(what, activation));
     const int dt = FSDP_BF16;
     const Operand ox = {"x", x, x_stride, dt, tokens, false, false}, og = {"w_gate", w_gate, w_gate_stride, dt, inner, false, false},
@@ -338,6 +357,7 @@ int fsdp_gated_ffn_grad_workspace(int64_t tokens, int64_t hidden, int64_t inner,
     clear_error();
     if (!bytes) return bad(what, "bytes is NULL");
     FSDP_TRY(check_product(what, {tokens, hidden, inner}));
+    FSDP_TRY(check_terms(what, {tokens, hidden, inner}));
     *bytes = ffn_grad_most_bytes(tokens, hidden, inner, aligned != 0);
     return FSDP_OK;
 }
@@ -352,6 +372,7 @@ int fsdp_gated_ffn_grad(int64_t tokens, int64_t hidden, int64_t inner, const voi
     const char* what = "gated_ffn_grad";
     clear_error();
     FSDP_TRY(check_product(what, {tokens, hidden, inner}));
+    FSDP_TRY(check_terms(what, {tokens, hidden, inner}));
     FSDP_TRY(check_activation(what, activation));
     const int dt = FSDP_BF16;
     const Operand og = {"grad_out", grad_out, grad_out_stride, dt, tokens, false, false}, ox = {"x", x, x_stride, dt, tokens, false, false},
@@ -378,7 +399,7 @@ int fsdp_orthogonalize_workspace(int64_t rows, int64_t cols, size_t* bytes) {
     const char* what = "orthogonalize_workspace";
     clear_error();
     if (!bytes) return bad(what, "bytes is NULL");
-    FSDP_TRY(check_product(what, {rows, cols}));
+    FSDP_TRY(check_ortho_size(what, rows, cols));
     *bytes = ortho_bytes(rows, cols);
     return FSDP_OK;
 }
@@ -388,7 +409,7 @@ int fsdp_orthogonalize(int64_t rows, int64_t cols, int dt, const void* x, int64_
                        size_t workspace_bytes, fsdp_stream_t stream) {
     const char* what = "orthogonalize";
     clear_error();
-    FSDP_TRY(check_product(what, {rows, cols}));
+    FSDP_TRY(check_ortho_size(what, rows, cols));
     const Operand ox = {"x", x, x_stride, dt, rows, false, false}, oo = {"out", out, out_stride, FSDP_BF16, rows, true, false};
     FSDP_TRY(check_operands(what, cols, {ox, oo}));
     FSDP_TRY(check_apart(what, {ox, oo}));

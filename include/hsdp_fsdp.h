@@ -518,8 +518,11 @@ int fsdp_layer_norm_grad(int64_t rows, int64_t cols, int dt, const void* grad_ou
  *   - Waits: the kernels wait inside, between their own warps. Every wait is
  *     bounded; one that ran out leaves the call's results undefined and shows
  *     in fsdp_operators_status.
- *   - Sizes below 2^31 - 2^9; a call enqueues up to 6 * steps + 2 kernels
- *     (orthogonalisation) or up to 6 (the others). */
+ *   - Sizes below 2^31 - 2^9, and sums of up to 2^24 terms: hidden and inner, the
+ *     tokens of a gradient (more go in several calls that accumulate), both
+ *     sides of a matrix that has more than 64 rows and columns.
+ *   - A call enqueues up to 6 * steps + 2 kernels (orthogonalisation) or up to 6
+ *     (the others). */
 
 enum fsdp_activation {
   FSDP_SILU = 0, /* z / (1 + exp(-z)) */
