@@ -153,12 +153,21 @@ int check_activation(const char* what, int act) {
     return act == FSDP_SILU || act == FSDP_GELU || act == FSDP_RELU ? FSDP_OK : bad(what, "unknown activation");
 }
 
-// No output may be another operand's memory.
-int check_apart(const char* what, std::initializer_list<Operand> ops) {
-    for (const Operand& o : ops)
-        if (o.output && o.data)
-            for (const Operand& p : ops)
-                if (&p != &o && p.data == o.data) return bad(what, std::string(o.name) + " is another operand's memory");
+// Operands of as many columns each.
+struct Operands {
+    int64_t cols;
+    std::initializer_list<Operand> list;
+};
+
+// No output may be another operand's memory; what holds no element is no memory.
+int check_apart(const char* what, std::initializer_list<Operands> groups) {
+    const auto holds = [](const Operand& o, int64_t cols) { return o.data && o.rows > 0 && cols > 0; };
+    for (const Operands& g : groups)
+        for (const Operand& o : g.list)
+            if (o.output && holds(o, g.cols))
+                for (const Operands& h : groups)
+                    for (const Operand& p : h.list)
+                        if (&p != &o && holds(p, h.cols) && p.data == o.data) return bad(what, std::string(o.name) + " is another operand's memory");
     return FSDP_OK;
 }
 
@@ -344,7 +353,7 @@ int fsdp_gated_ffn(int64_t tokens, int64_t hidden, int64_t inner, const void* x,
     FSDP_TRY(check_operands(what, hidden, {ox, og, ou, oo}));
     FSDP_TRY(check_operands(what, inner, {od, kg, ku}));
     if (tokens > 0 && inner > 0 && !gate != !up) return bad(what, "gate and up: one of them is NULL");
-    FSDP_TRY(check_apart(what, {ox, og, ou, od, kg, ku, oo}));
+    FSDP_TRY(check_apart(what, {{hidden, {ox, og, ou, oo}}, {inner, {od, kg, ku}}}));
     const FfnArgs a = {tokens, hidden, inner, activation, mat(x, x_stride), mat(w_gate, w_gate_stride), mat(w_up, w_up_stride),
                        mat(w_down, w_down_stride), mat(gate, gate_stride), mat(up, up_stride), mat(out, out_stride),
                        static_cast<char*>(workspace)};
@@ -386,7 +395,7 @@ int fsdp_gated_ffn_grad(int64_t tokens, int64_t hidden, int64_t inner, const voi
                   gd = {"grad_w_down", grad_w_down, grad_w_down_stride, param_grad_dt, hidden, true, false};
     FSDP_TRY(check_operands(what, hidden, {og, ox, wg, wu, gx, gg, gu}));
     FSDP_TRY(check_operands(what, inner, {wd, kg, ku, gd}));
-    FSDP_TRY(check_apart(what, {og, ox, wg, wu, wd, kg, ku, gx, gg, gu, gd}));
+    FSDP_TRY(check_apart(what, {{hidden, {og, ox, wg, wu, gx, gg, gu}}, {inner, {wd, kg, ku, gd}}}));
     const FfnGradArgs a = {tokens, hidden, inner, activation, accumulate ? 1 : 0, mat(grad_out, grad_out_stride), mat(x, x_stride),
                            mat(w_gate, w_gate_stride), mat(w_up, w_up_stride), mat(w_down, w_down_stride), mat(gate, gate_stride),
                            mat(up, up_stride), mat(grad_x, grad_x_stride), mat(grad_w_gate, grad_w_gate_stride),
@@ -412,7 +421,7 @@ int fsdp_orthogonalize(int64_t rows, int64_t cols, int dt, const void* x, int64_
     FSDP_TRY(check_ortho_size(what, rows, cols));
     const Operand ox = {"x", x, x_stride, dt, rows, false, false}, oo = {"out", out, out_stride, FSDP_BF16, rows, true, false};
     FSDP_TRY(check_operands(what, cols, {ox, oo}));
-    FSDP_TRY(check_apart(what, {ox, oo}));
+    FSDP_TRY(check_apart(what, {{cols, {ox, oo}}}));
     if (steps < 1 || steps > 64) return bad(what, "steps is not in [1, 64]");
     for (const double v : {a, b, c})
         if (!(std::fabs(v) <= 256.0)) return bad(what, "a coefficient is not in [-256, 256]");

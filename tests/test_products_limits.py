@@ -40,3 +40,15 @@ def test_workspaces():
     refused(L.fsdp_orthogonalize_workspace(65, LONG + 1, b), "sum", "2^24")
     assert L.fsdp_gated_ffn_workspace(LONG + 1, 8, 8, 1, b) == C.FSDP_OK
     assert L.fsdp_orthogonalize_workspace(64, 2 ** 31 - 513, b) == C.FSDP_OK
+
+
+def test_operands_without_elements_overlap_nothing():
+    # no tokens, or no columns, on views of one buffer
+    assert ffn(t=0, x=P, out=P, g=P, gs=16, u=P, us=16, work=None, wb=0) == C.FSDP_OK
+    assert ffn(t=0, h=0, x=P, wg=P, wu=P, wd=P, out=P, work=None, wb=0) == C.FSDP_OK
+    assert ortho(r=0, x=P, out=P, work=None, wb=0) == C.FSDP_OK
+    assert ortho(c=0, x=P, out=P, work=None, wb=0) == C.FSDP_OK
+    # those that hold elements do
+    refused(ffn(t=1, x=P, out=P), "out", "another operand")
+    refused(ffn(t=3, f=0, g=P, u=P, out=P), "out", "another operand")
+    refused(grad(t=0, dg=9 * P, du=9 * P), "another operand")
