@@ -10,8 +10,9 @@
 // the 2-norm, a few strong directions over 3% or 0.1% of noise: 0.002; with
 // one plane 0.02 and 0.04; in bfloat16 0.17 and 0.34. Noise alone 0.002, 0.002
 // and 0.011. Rounding the result to bfloat16 alone is 0.0017.) In the last two
-// steps the singular values are near one, and a shift near one leaves the
-// product the smaller part.
+// steps the singular values are near one, and so is the whole polynomial: with
+// shift = a the product would bring a - 1 times X that has to go again, so shift
+// is (1 + a) / 2 there, which halves that.
 #include <algorithm>
 #include <cmath>
 #include <utility>
