@@ -548,11 +548,22 @@ inline int64_t tiles_of(const Product& p, int width) {
     return whole + tn;  // the last row of tiles holds all columns
 }
 inline Cut cut_of(const Product& p, bool may_split) {
-    // a tile half as wide takes half the time and a little more
+    // A tile half as wide is taken for 0.55 of a wide one. Measured, a wave of
+    // them takes 0.5 to 0.7 of the time where the epilogue or a tile's start is
+    // most of it (GatedGrad of 517 x 2048 33 us and 54, Gram of 1111 x 2049 17
+    // and 24), and 0.7 to 0.8 where the products are, so near the border this is
+    // too kind to slim tiles (4096 x 4096 x 4096 in 7 waves 113 us, 82 in 4 wide
+    // ones) and right on either side of it (4096 x 11008, 10 wide waves 213 us
+    // and 19 slim ones 305; 48 x 8192, one wave each, 129 and 108).
     const int64_t wide = tiles_of(p, 256), slim = tiles_of(p, 128);
     const double w = (double)tiles_over(wide, kPairs), s = 0.55 * (double)tiles_over(slim, kPairs);
     Cut c = {w <= s ? 256 : 128, 1, 0};
     const int64_t steps = tiles_over(p.k[0], kStep) + (p.terms > 1 ? tiles_over(p.k[1], kStep) : 0);
+    // Parts of at least 8 steps, where they bring twice as many pairs to work: the
+    // last product of one token, 32 tiles of 172 steps, takes 57 us whole, 41 in
+    // parts and 3 to join them. Shorter ones lose (128 x 384, three products of 27
+    // us whole, 21 in parts and 8 to join); those of 39 to 76 tiles are left whole,
+    // though long ones would gain. In parts a symmetric product computes all tiles.
     Product full = p;
     full.symmetric = 0;
     const int64_t tiles = tiles_of(full, c.width);

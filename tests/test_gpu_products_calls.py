@@ -135,3 +135,28 @@ def test_batches_of_sequences():
     C.fsdp_gated_ffn(x, *w, y, work, gate=g, up=u)
     for k, v in R.gated_ffn(x.view(6, 64), *w, "silu").items():
         R.agree(k, {"out": y, "gate": g, "up": u}[k].view(6, -1), v)
+
+
+def test_rows_that_overlap():
+    # inputs of stride 0 (every row the same) and of rows that lie inside one another
+    t, h, f = 70, 72, 136
+    def over(seed, rows, cols, stride, std):  # noqa: E306
+        return torch.as_strided(rand(seed, 1, (rows - 1) * stride + cols, std)[0], (rows, cols), (stride, 1))
+    for stride in (0, 1, 8, 24):
+        x, grad = over(1, t, h, stride, 1.0), over(2, t, h, stride, 0.1)
+        w = [over(3, f, h, stride, 0.1), over(4, f, h, stride, 0.1), over(5, h, f, stride, 0.1)]
+        g, u = over(6, t, f, stride, 1.0), over(7, t, f, stride, 1.0)
+        y, dx, dw = torch.empty(t, h, dtype=BF16, device="cuda"), torch.empty(t, h, dtype=BF16, device="cuda"), [torch.empty(v.shape, dtype=BF16, device="cuda") for v in w]
+        work = torch.empty(C.fsdp_gated_ffn_grad_workspace(t, h, f, aligned=False), dtype=torch.uint8, device="cuda")
+        C.fsdp_gated_ffn(x, *w, y, work)
+        R.agree("out", y, R.gated_ffn(x, *w, "silu")["out"])
+        C.fsdp_gated_ffn_grad(grad, x, *w, g, u, dx, *dw, work)
+        want = R.gated_ffn_grad(grad, x, *w, g, u, "silu")
+        for k, v in zip(("x", "w_gate", "w_up", "w_down"), [dx, *dw]):
+            R.agree(k, v, want[k])
+        for rows, cols in [(40, 100), (100, 130)]:
+            m = over(8, rows, cols, stride, 1.0)
+            o = torch.empty(rows, cols, dtype=BF16, device="cuda")
+            work = torch.empty(C.fsdp_orthogonalize_workspace(rows, cols), dtype=torch.uint8, device="cuda")
+            C.fsdp_orthogonalize(m, o, work)
+            assert R.distance(o, R.orthogonalize(m)) < 2.3e-3 + 5 * 2.0 ** -11
