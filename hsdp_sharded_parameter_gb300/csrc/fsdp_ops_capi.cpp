@@ -133,8 +133,9 @@ int check_product(const char* what, std::initializer_list<int64_t> sizes) {
 }
 
 // A tile's sum over k runs in one go, in binary32, and the warps that wait for it
-// wait two seconds: 2^24 terms, two products of which are added at most, take
-// 0.4 s where all SMs share the memory.
+// wait two seconds: at 2^24 terms, two products of which are added at most, it
+// takes 0.4 s where all SMs share the memory (a gradient of 2^24 tokens, 8 x 8,
+// 0.07 s in all).
 constexpr int64_t kMostTerms = (int64_t)1 << 24;
 
 int check_terms(const char* what, std::initializer_list<int64_t> lengths) {

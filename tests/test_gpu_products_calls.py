@@ -160,3 +160,28 @@ def test_rows_that_overlap():
             work = torch.empty(C.fsdp_orthogonalize_workspace(rows, cols), dtype=torch.uint8, device="cuda")
             C.fsdp_orthogonalize(m, o, work)
             assert R.distance(o, R.orthogonalize(m)) < 2.3e-3 + 5 * 2.0 ** -11
+
+
+def test_the_longest_sums():
+    # a sum of n random terms of size s wanders some 6 sqrt(n) s away from 0 at most; each of n / 16 additions
+    # may cut 2^-21 of that, beside the terms' magnitudes' sum, 0.6 n s, (1 / 16) 2^-21 6 sqrt(n) / 0.6 = 2^-9.7
+    n = 2 ** 24
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").to(BF16)  # noqa: E731
+    x, grad, gate, up, w = r(n, 8), r(n, 8), r(n, 8), r(n, 8), [r(8, 8), r(8, 8), r(8, 8)]
+    dx, dw = torch.empty_like(x), [torch.empty(8, 8, device="cuda") for _ in w]
+    work = torch.empty(C.fsdp_gated_ffn_grad_workspace(n, 8, 8), dtype=torch.uint8, device="cuda")
+    C.fsdp_gated_ffn_grad(grad, x, *w, gate, up, dx, *dw, work, "relu")
+    h = (gate.double().clamp(min=0) * up.double()).to(BF16).double()
+    d = (grad.double() @ w[2].double())
+    du, dg = (d * gate.double().clamp(min=0)).to(BF16).double(), (d * up.double() * (gate > 0)).to(BF16).double()
+    for got, a, b in [(dw[0], dg, x.double()), (dw[1], du, x.double()), (dw[2], grad.double(), h)]:
+        assert bool(((got.double() - a.T @ b).abs() <= 2.0 ** -9 * (a.abs().T @ b.abs())).all())
+    y = torch.empty(3, 8, dtype=BF16, device="cuda")
+    wide = [r(n, 8), r(n, 8), r(8, n)]
+    work = torch.empty(C.fsdp_gated_ffn_workspace(3, 8, n), dtype=torch.uint8, device="cuda")
+    C.fsdp_gated_ffn(x[:3], *wide, y, work, "relu")
+    h = ((x[:3].double() @ wide[0].double().T).clamp(min=0) * (x[:3].double() @ wide[1].double().T))
+    # beside that h's rounding, 2^-8 of it
+    assert bool(((y.double() - h @ wide[2].double().T).abs() <= (2.0 ** -9 + 2.0 ** -8) * (h.abs() @ wide[2].double().abs().T)).all())
